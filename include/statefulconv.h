@@ -291,6 +291,80 @@ sc_status sc_cca_qk_conv(const sc_cca_desc* desc, const void* q, const void* k,
                          const uint8_t* prefill_has_initial_state,
                          int64_t num_tokens, void* stream);
 
+/* Gated delta rule (GDN page "vllm.model_executor.layers.mamba.ops.cpu.
+ * gdn_attention": the recurrence that consumes the mixed-qkv conv's output, as
+ * decode, speculative decode and varlen prefill, with the gates computed from
+ * A_log, a, b and dt_bias). Per value head, with a state S (DV x DK) that lives
+ * in a slot pool next to the conv state:
+ *   g = -exp(A_log) * softplus(a + dt_bias),  beta = sigmoid(b)
+ *   q^, k^ = q, k scaled by 1/sqrt(sum of squares + 1e-6) (qk_l2norm = 1), or as they are
+ *   S <- exp(g) S;  S <- S + beta (v - S k^) k^T;  out = scale * S q^
+ * Value head h reads key head h / (num_v_heads / num_k_heads). q, k, v and out
+ * are bf16 (the page's core rejects other inputs); the state, the gates and
+ * every sum are fp32.
+ *   q, k    (T, num_k_heads * DK), v, out (T, num_v_heads * DV): rows of their
+ *           strides, e.g. the column blocks of the conv's output rows; q and k
+ *           16-byte aligned with strides a multiple of 8
+ *   a, b    (T, num_v_heads), gate_dtype; A_log, dt_bias (num_v_heads) fp32
+ *   state   (num_slots, num_v_heads, DV, DK) fp32, contiguous, 16-byte aligned
+ * DK is 64 or 128, DV a multiple of 16 (SC_ERR_UNSUPPORTED otherwise; also
+ * for rows that break the alignment above). */
+typedef struct {
+  int32_t num_k_heads;   /* HK >= 1 */
+  int32_t num_v_heads;   /* HV, a multiple of HK */
+  int32_t head_k_dim;    /* DK */
+  int32_t head_v_dim;    /* DV */
+  int32_t dtype;         /* SC_DTYPE_BF16 */
+  int32_t gate_dtype;    /* sc_dtype of a and b */
+  int32_t qk_l2norm;     /* 0 or 1 */
+  float scale;           /* finite; the usual choice is 1/sqrt(DK) */
+  int64_t q_row_stride, k_row_stride, v_row_stride;   /* elements */
+  int64_t a_row_stride, b_row_stride, out_row_stride;
+  int64_t state_indices_stride;                       /* >= 1 */
+} sc_gdn_desc;
+
+/* Bytes of workspace sc_gdn_prefill_varlen needs for these sizes (host only). */
+sc_status sc_gdn_workspace_bytes(const sc_gdn_desc* desc, int32_t batch, int64_t num_tokens,
+                                 int64_t* bytes);
+
+/* Varlen prefill: request r owns token rows [qsl[r], qsl[r+1]), starts from
+ * state[slot] if has_initial_state[r] (zeros otherwise, and for a slot outside
+ * the pool) and leaves its final state there. A zero-length request leaves
+ * its slot untouched. Tokens are taken 64 at a time; a non-finite input can
+ * reach earlier rows of its own request's group of 64, and no other request.
+ *   workspace (device) 16-byte aligned, at least sc_gdn_workspace_bytes; its
+ *             contents are scratch, so two calls that may run at once (two
+ *             streams, two captured graphs) need one each. */
+sc_status sc_gdn_prefill_varlen(const sc_gdn_desc* desc, const void* q, const void* k,
+                                const void* v, const void* a, const void* b,
+                                const float* A_log, const float* dt_bias, void* out,
+                                float* state_pool, int32_t num_slots,
+                                const int32_t* query_start_loc, const int32_t* state_indices,
+                                const uint8_t* has_initial_state, int32_t batch,
+                                int64_t num_tokens, void* workspace, int64_t workspace_bytes,
+                                void* stream);
+
+/* Decode / multi-token update: `batch` requests of exactly q_len tokens,
+ * request r owning rows [r*q_len, (r+1)*q_len). has_initial_state NULL = every
+ * request continues its state. */
+sc_status sc_gdn_update(const sc_gdn_desc* desc, const void* q, const void* k, const void* v,
+                        const void* a, const void* b, const float* A_log, const float* dt_bias,
+                        void* out, float* state_pool, int32_t num_slots,
+                        const int32_t* state_indices, const uint8_t* has_initial_state,
+                        int32_t batch, int32_t q_len, void* stream);
+
+/* Speculative update: request r has q_len drafts and q_len state slots,
+ * state_indices[r*stride .. r*stride + q_len) (stride >= q_len). It starts from
+ * the slot of its last accepted draft, entry num_accepted_tokens[r] - 1
+ * (clamped to [0, q_len)), and leaves the state after draft t in entry t's
+ * slot, so that the next call can roll back to any of them. */
+sc_status sc_gdn_update_spec(const sc_gdn_desc* desc, const void* q, const void* k,
+                             const void* v, const void* a, const void* b, const float* A_log,
+                             const float* dt_bias, void* out, float* state_pool,
+                             int32_t num_slots, const int32_t* state_indices,
+                             const int32_t* num_accepted_tokens, int32_t batch, int32_t q_len,
+                             void* stream);
+
 /* Checks the device-side preconditions the calls above document but cannot
  * check without a host sync (a debugging and test aid, not for the hot path):
  * waits for `stream`, copies the metadata to the host and returns

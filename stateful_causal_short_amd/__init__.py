@@ -28,8 +28,9 @@ SC_STATE_DS, SC_STATE_SD = 0, 1
 
 EXPORTS = ("sc_conv_prefill_varlen", "sc_conv_update", "sc_conv_update_spec",
            "sc_conv_update_spec_varlen", "sc_validate_metadata", "sc_state_gather",
-           "sc_state_scatter", "sc_cca_qk_conv", "sc_status_string",
-           "sc_abi_version")
+           "sc_state_scatter", "sc_cca_qk_conv", "sc_gdn_workspace_bytes",
+           "sc_gdn_prefill_varlen", "sc_gdn_update", "sc_gdn_update_spec",
+           "sc_status_string", "sc_abi_version")
 
 
 class ScError(RuntimeError):
@@ -66,6 +67,17 @@ class sc_cca_desc(ctypes.Structure):
                 ("v_cur_row_stride", ctypes.c_int64), ("v_del_row_stride", ctypes.c_int64),
                 ("out_row_stride", ctypes.c_int64), ("decode_slot_stride", ctypes.c_int64),
                 ("prefill_slot_stride", ctypes.c_int64)]
+
+
+class sc_gdn_desc(ctypes.Structure):
+    _fields_ = [("num_k_heads", ctypes.c_int32), ("num_v_heads", ctypes.c_int32),
+                ("head_k_dim", ctypes.c_int32), ("head_v_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32),
+                ("qk_l2norm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+                ("v_row_stride", ctypes.c_int64), ("a_row_stride", ctypes.c_int64),
+                ("b_row_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
+                ("state_indices_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -108,6 +120,16 @@ def lib():
         L.sc_cca_qk_conv.restype = I32
         L.sc_cca_qk_conv.argtypes = [ctypes.POINTER(sc_cca_desc), P, P, P, P, P, P, P,
                                      P, P, P, P, P, I32, I32, P, I32, P, P, P, I64, P]
+        G = ctypes.POINTER(sc_gdn_desc)
+        L.sc_gdn_workspace_bytes.restype = I32
+        L.sc_gdn_workspace_bytes.argtypes = [G, I32, I64, ctypes.POINTER(I64)]
+        L.sc_gdn_prefill_varlen.restype = I32
+        L.sc_gdn_prefill_varlen.argtypes = [G, P, P, P, P, P, P, P, P, P, I32, P, P, P, I32,
+                                            I64, P, I64, P]
+        L.sc_gdn_update.restype = I32
+        L.sc_gdn_update.argtypes = [G, P, P, P, P, P, P, P, P, P, I32, P, P, I32, I32, P]
+        L.sc_gdn_update_spec.restype = I32
+        L.sc_gdn_update_spec.argtypes = [G, P, P, P, P, P, P, P, P, P, I32, P, P, I32, I32, P]
         L.sc_status_string.restype = ctypes.c_char_p
         L.sc_status_string.argtypes = [I32]
         L.sc_abi_version.restype = I32
@@ -510,3 +532,161 @@ __all__ = ["lib", "ScError", "LIB_PATH", "EXPORTS", "sc_conv_desc", "sc_ckpt_des
            "sc_cca_desc", "sc_conv_fuse", "sc_conv_prefill_varlen", "sc_conv_update",
            "sc_conv_update_spec", "sc_conv_update_spec_varlen", "sc_validate_metadata",
            "sc_state_gather", "sc_state_scatter", "sc_cca_qk_conv"]
+
+
+def _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices, scale,
+              qk_l2norm):
+    """Descriptor of a gated delta rule call; the heads follow from the pool's
+    shape (num_slots, HV, DV, DK) and the width of query."""
+    torch = _torch()
+    if state_pool.dim() != 4 or state_pool.dtype != torch.float32 or \
+            not state_pool.is_contiguous():
+        raise ValueError("state_pool: expected a contiguous float32 (num_slots, HV, DV, DK) "
+                         "tensor")
+    _, hv, dv, dk = state_pool.shape
+    strides = [_rows(t, n) for n, t in (("query", query), ("key", key), ("value", value),
+                                        ("a", a), ("b", b), ("out", out))]
+    if dk < 1 or query.shape[1] % dk or query.shape[1] == 0 or key.shape[1] != query.shape[1]:
+        raise ValueError(f"query, key: expected rows of HK * {dk} values")
+    if value.shape[1] != hv * dv or out.shape[1] != hv * dv:
+        raise ValueError(f"value, out: expected rows of {hv} * {dv} values")
+    if a.shape[1] != hv or b.shape[1] != hv:
+        raise ValueError(f"a, b: expected rows of {hv} values")
+    rows = query.shape[0]
+    for name, t in (("key", key), ("value", value), ("a", a), ("b", b), ("out", out)):
+        if t.shape[0] < rows:
+            raise ValueError(f"{name}: {t.shape[0]} rows for {rows} tokens")
+    for name, t in (("key", key), ("value", value), ("out", out)):
+        if t.dtype != query.dtype:
+            raise ValueError(f"{name}: dtype {t.dtype} differs from query's {query.dtype}")
+    if a.dtype != b.dtype:
+        raise ValueError("a, b: expected one dtype")
+    for name, t in (("A_log", A_log), ("dt_bias", dt_bias)):
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != hv:
+            raise ValueError(f"{name}: expected a contiguous float32 tensor of {hv} entries")
+    return sc_gdn_desc(
+        num_k_heads=query.shape[1] // dk, num_v_heads=hv, head_k_dim=dk, head_v_dim=dv,
+        dtype=_dtype_code(query), gate_dtype=_dtype_code(a), qk_l2norm=1 if qk_l2norm else 0,
+        scale=dk ** -0.5 if scale is None else scale, q_row_stride=strides[0],
+        k_row_stride=strides[1], v_row_stride=strides[2], a_row_stride=strides[3],
+        b_row_stride=strides[4], out_row_stride=strides[5],
+        state_indices_stride=_index_stride(state_indices, "state_indices"))
+
+
+def _workspace(workspace, need, like, stream):
+    """The given workspace, or a new one of `need` bytes from torch's allocator
+    (on the call's stream: freed memory is not reused before the call has run)."""
+    torch = _torch()
+    if workspace is None:
+        if need == 0:
+            return None
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor on the call's device")
+    return workspace
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def sc_gdn_workspace_bytes(num_tokens: int, batch: int, *, num_k_heads: int, num_v_heads: int,
+                           head_k_dim: int, head_v_dim: int) -> int:
+    """Bytes of workspace that sc_gdn_prefill_varlen needs for a batch of
+    `batch` requests with `num_tokens` tokens in all."""
+    kw, vw = num_k_heads * head_k_dim, num_v_heads * head_v_dim
+    desc = sc_gdn_desc(num_k_heads=num_k_heads, num_v_heads=num_v_heads, head_k_dim=head_k_dim,
+                       head_v_dim=head_v_dim, dtype=SC_DTYPE_BF16, gate_dtype=SC_DTYPE_BF16,
+                       qk_l2norm=1, scale=1.0, q_row_stride=kw, k_row_stride=kw,
+                       v_row_stride=vw, a_row_stride=num_v_heads, b_row_stride=num_v_heads,
+                       out_row_stride=vw, state_indices_stride=1)
+    return _gdn_need(desc, batch, num_tokens)
+
+
+def _gdn_need(desc, batch, num_tokens) -> int:
+    n = ctypes.c_int64(0)
+    _check("sc_gdn_workspace_bytes",
+           lib().sc_gdn_workspace_bytes(ctypes.byref(desc), batch, num_tokens, ctypes.byref(n)))
+    return n.value
+
+
+def sc_gdn_prefill_varlen(query, key, value, a, b, A_log, dt_bias, out, state_pool,
+                          query_start_loc, state_indices, has_initial_state, *,
+                          scale: Optional[float] = None, qk_l2norm: bool = True,
+                          workspace=None, stream=None):
+    """Gated delta rule over a varlen batch; updates ``state_pool`` in place.
+
+    query, key: (T, HK * DK) bf16; value, out: (T, HV * DV) bf16 (column blocks
+    of the conv's output rows will do); a, b: (T, HV) bf16 or fp32; A_log,
+    dt_bias: (HV) fp32; state_pool: (num_slots, HV, DV, DK) fp32;
+    query_start_loc int32 (B+1); state_indices int32 (B) or column 0 of (B, n);
+    has_initial_state bool/uint8 (B). scale defaults to DK ** -0.5.
+    workspace: None, or a tensor of sc_gdn_workspace_bytes bytes to reuse
+    (one for each call that may run at the same time).
+    """
+    torch = _torch()
+    if query_start_loc.dtype != torch.int32 or not query_start_loc.is_contiguous() or \
+            query_start_loc.dim() != 1 or query_start_loc.shape[0] < 1:
+        raise ValueError("query_start_loc: expected a contiguous int32 tensor of batch + 1 "
+                         "entries")
+    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
+                     scale, qk_l2norm)
+    batch, T = query_start_loc.shape[0] - 1, query.shape[0]
+    _covers(batch, state_indices=state_indices, has_initial_state=has_initial_state)
+    raw = _stream(stream, query)
+    workspace = _workspace(workspace, _gdn_need(desc, batch, T), query, stream)
+    st = lib().sc_gdn_prefill_varlen(
+        ctypes.byref(desc), _ptr(query), _ptr(key), _ptr(value), _ptr(a), _ptr(b), _ptr(A_log),
+        _ptr(dt_bias), _ptr(out), _ptr(state_pool), state_pool.shape[0], _ptr(query_start_loc),
+        _ptr(state_indices), _flags(has_initial_state, "has_initial_state"), batch, T,
+        _ptr(workspace), _nbytes(workspace), raw)
+    _check("sc_gdn_prefill_varlen", st)
+
+
+def sc_gdn_update(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
+                  has_initial_state=None, *, q: int = 1, scale: Optional[float] = None,
+                  qk_l2norm: bool = True, stream=None):
+    """Gated delta rule for `q` tokens of each request (rows [r*q, (r+1)*q));
+    updates ``state_pool`` in place. Tensors as for sc_gdn_prefill_varlen."""
+    if q < 1 or query.shape[0] % q:
+        raise ValueError("rows must be a multiple of q >= 1")
+    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
+                     scale, qk_l2norm)
+    batch = query.shape[0] // q
+    _covers(batch, state_indices=state_indices, has_initial_state=has_initial_state)
+    st = lib().sc_gdn_update(
+        ctypes.byref(desc), _ptr(query), _ptr(key), _ptr(value), _ptr(a), _ptr(b), _ptr(A_log),
+        _ptr(dt_bias), _ptr(out), _ptr(state_pool), state_pool.shape[0], _ptr(state_indices),
+        _flags(has_initial_state, "has_initial_state"), batch, q, _stream(stream, query))
+    _check("sc_gdn_update", st)
+
+
+def sc_gdn_update_spec(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
+                       num_accepted_tokens, *, q: int, scale: Optional[float] = None,
+                       qk_l2norm: bool = True, stream=None):
+    """Speculative gated delta rule: request r has q drafts (rows [r*q, (r+1)*q))
+    and q state slots, state_indices int32 (B, q). It starts from the slot of its
+    last accepted draft (entry num_accepted_tokens[r] - 1; int32 (B)) and leaves
+    the state after draft t in slot t's row."""
+    torch = _torch()
+    if q < 1 or query.shape[0] % q:
+        raise ValueError("rows must be a multiple of q >= 1")
+    if state_indices.dim() != 2 or state_indices.shape[1] < q or \
+            (state_indices.shape[1] > 1 and state_indices.numel() and
+             state_indices.stride(1) != 1):
+        raise ValueError("state_indices: expected (B, q) with adjacent entries")
+    if num_accepted_tokens.dtype != torch.int32 or not num_accepted_tokens.is_contiguous():
+        raise ValueError("num_accepted_tokens: expected a contiguous int32 tensor")
+    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
+                     scale, qk_l2norm)
+    batch = query.shape[0] // q
+    if batch <= 1:
+        desc.state_indices_stride = state_indices.shape[1]
+    _covers(batch, state_indices=state_indices, num_accepted_tokens=num_accepted_tokens)
+    st = lib().sc_gdn_update_spec(
+        ctypes.byref(desc), _ptr(query), _ptr(key), _ptr(value), _ptr(a), _ptr(b), _ptr(A_log),
+        _ptr(dt_bias), _ptr(out), _ptr(state_pool), state_pool.shape[0], _ptr(state_indices),
+        _ptr(num_accepted_tokens), batch, q, _stream(stream, query))
+    _check("sc_gdn_update_spec", st)

@@ -3,6 +3,7 @@
 // in include/statefulconv.h.
 #include <stdint.h>
 
+#include <cmath>
 #include <new>
 #include <unordered_set>
 #include <vector>
@@ -10,6 +11,7 @@
 #include "statefulconv.h"
 #include "kernels.hpp"
 #include "cca.hpp"
+#include "gdn.hpp"
 
 namespace {
 
@@ -100,6 +102,72 @@ sc_status validate_metadata_host(const int32_t* query_start_loc,
       if (v >= num_slots || !seen.insert(v).second) return SC_ERR_INVALID_ARG;
     }
   }
+  return SC_OK;
+}
+
+// Descriptor checks shared by the gated delta rule entry points.
+sc_status check_gdn_desc(const sc_gdn_desc* d) {
+  if (d->dtype != SC_DTYPE_BF16) return SC_ERR_DTYPE;
+  if (d->gate_dtype != SC_DTYPE_F32 && d->gate_dtype != SC_DTYPE_BF16) return SC_ERR_DTYPE;
+  if (d->num_k_heads < 1 || d->num_v_heads < 1 || d->num_v_heads % d->num_k_heads != 0 ||
+      d->head_k_dim < 1 || d->head_v_dim < 1)
+    return SC_ERR_INVALID_ARG;
+  if (d->qk_l2norm != 0 && d->qk_l2norm != 1) return SC_ERR_INVALID_ARG;
+  if (!std::isfinite(d->scale)) return SC_ERR_INVALID_ARG;
+  const int64_t kw = (int64_t)d->num_k_heads * d->head_k_dim;
+  const int64_t vw = (int64_t)d->num_v_heads * d->head_v_dim;
+  if (d->q_row_stride < kw || d->k_row_stride < kw || d->v_row_stride < vw ||
+      d->out_row_stride < vw || d->a_row_stride < d->num_v_heads ||
+      d->b_row_stride < d->num_v_heads || d->state_indices_stride < 1)
+    return SC_ERR_INVALID_ARG;
+  if ((d->head_k_dim != 64 && d->head_k_dim != 128) || d->head_v_dim % 16 != 0 ||
+      d->q_row_stride % 8 != 0 || d->k_row_stride % 8 != 0)
+    return SC_ERR_UNSUPPORTED;
+  // a head's state and a row of heads are addressed with 32-bit offsets
+  if (vw > (1 << 24) || kw > (1 << 24)) return SC_ERR_UNSUPPORTED;
+  return SC_OK;
+}
+
+int64_t gdn_chunks(int32_t batch, int64_t num_tokens) {
+  return num_tokens / sc::kGdnChunk + batch;
+}
+
+// Pointers and sizes common to the three calls.
+sc_status gdn_args(const sc_gdn_desc* d, const void* q, const void* k, const void* v,
+                   const void* a, const void* b, const float* A_log, const float* dt_bias,
+                   void* out, float* pool, int32_t num_slots, const int32_t* slots,
+                   int32_t batch, sc::GdnArgs* g) {
+  if (!q || !k || !v || !a || !b || !A_log || !dt_bias || !out || !slots || (!pool && num_slots > 0))
+    return SC_ERR_NULL_ARG;
+  if (out == q || out == k || out == v) return SC_ERR_INVALID_ARG;
+  if (!al16(q) || !al16(k) || !al16(pool)) return SC_ERR_UNSUPPORTED;
+  *g = sc::GdnArgs{};
+  g->q = q;
+  g->k = k;
+  g->v = v;
+  g->a = a;
+  g->b = b;
+  g->A_log = A_log;
+  g->dt_bias = dt_bias;
+  g->out = out;
+  g->pool = pool;
+  g->slots = slots;
+  g->q_rs = d->q_row_stride;
+  g->k_rs = d->k_row_stride;
+  g->v_rs = d->v_row_stride;
+  g->a_rs = d->a_row_stride;
+  g->b_rs = d->b_row_stride;
+  g->out_rs = d->out_row_stride;
+  g->slot_stride = d->state_indices_stride;
+  g->scale = d->scale;
+  g->hk = d->num_k_heads;
+  g->hv = d->num_v_heads;
+  g->dk = d->head_k_dim;
+  g->dv = d->head_v_dim;
+  g->l2norm = d->qk_l2norm;
+  g->gate_f32 = d->gate_dtype == SC_DTYPE_F32;
+  g->num_slots = num_slots;
+  g->batch = batch;
   return SC_OK;
 }
 
@@ -430,6 +498,97 @@ sc_status sc_cca_qk_conv(const sc_cca_desc* desc, const void* q, const void* k,
   a.num_decodes = num_decodes;
   a.num_prefills = num_prefills;
   return from_hip(sc::launch_cca(a, (hipStream_t)stream));
+}
+
+sc_status sc_gdn_workspace_bytes(const sc_gdn_desc* desc, int32_t batch, int64_t num_tokens,
+                                 int64_t* bytes) {
+  if (!desc || !bytes) return SC_ERR_NULL_ARG;
+  sc_status st = check_gdn_desc(desc);
+  if (st != SC_OK) return st;
+  if (batch < 0 || num_tokens < 0) return SC_ERR_INVALID_ARG;
+  if (num_tokens > 0x7FFFFFFFLL) return SC_ERR_UNSUPPORTED;
+  *bytes = batch == 0 || num_tokens == 0
+               ? 0
+               : sc::GdnWorkspace::bytes(gdn_chunks(batch, num_tokens), desc->num_k_heads,
+                                         desc->num_v_heads, desc->head_k_dim);
+  return SC_OK;
+}
+
+sc_status sc_gdn_prefill_varlen(const sc_gdn_desc* desc, const void* q, const void* k,
+                                const void* v, const void* a, const void* b,
+                                const float* A_log, const float* dt_bias, void* out,
+                                float* state_pool, int32_t num_slots,
+                                const int32_t* query_start_loc, const int32_t* state_indices,
+                                const uint8_t* has_initial_state, int32_t batch,
+                                int64_t num_tokens, void* workspace, int64_t workspace_bytes,
+                                void* stream) {
+  if (!desc) return SC_ERR_NULL_ARG;
+  sc_status st = check_gdn_desc(desc);
+  if (st != SC_OK) return st;
+  if (batch < 0 || num_tokens < 0 || num_slots < 0 || workspace_bytes < 0)
+    return SC_ERR_INVALID_ARG;
+  if (batch == 0 || num_tokens == 0) return SC_OK;
+  if (num_tokens > 0x7FFFFFFFLL) return SC_ERR_UNSUPPORTED;
+  if (!query_start_loc || !has_initial_state || !workspace) return SC_ERR_NULL_ARG;
+  sc::GdnArgs g;
+  st = gdn_args(desc, q, k, v, a, b, A_log, dt_bias, out, state_pool, num_slots, state_indices,
+                batch, &g);
+  if (st != SC_OK) return st;
+  const int64_t chunks = gdn_chunks(batch, num_tokens);
+  if (chunks > 0x7FFFFFFFLL) return SC_ERR_UNSUPPORTED;
+  if (!al16(workspace) ||
+      workspace_bytes < sc::GdnWorkspace::bytes(chunks, g.hk, g.hv, g.dk))
+    return SC_ERR_INVALID_ARG;
+  g.qsl = query_start_loc;
+  g.has_init = has_initial_state;
+  g.num_tokens = num_tokens;
+  g.ws = (char*)workspace;
+  g.n_chunks = (int32_t)chunks;
+  return from_hip(sc::launch_gdn_prefill(g, (hipStream_t)stream));
+}
+
+sc_status sc_gdn_update(const sc_gdn_desc* desc, const void* q, const void* k, const void* v,
+                        const void* a, const void* b, const float* A_log, const float* dt_bias,
+                        void* out, float* state_pool, int32_t num_slots,
+                        const int32_t* state_indices, const uint8_t* has_initial_state,
+                        int32_t batch, int32_t q_len, void* stream) {
+  if (!desc) return SC_ERR_NULL_ARG;
+  sc_status st = check_gdn_desc(desc);
+  if (st != SC_OK) return st;
+  if (batch < 0 || q_len < 0 || num_slots < 0) return SC_ERR_INVALID_ARG;
+  if (batch == 0 || q_len == 0) return SC_OK;
+  if ((int64_t)batch * q_len > 0x7FFFFFFFLL) return SC_ERR_UNSUPPORTED;
+  sc::GdnArgs g;
+  st = gdn_args(desc, q, k, v, a, b, A_log, dt_bias, out, state_pool, num_slots, state_indices,
+                batch, &g);
+  if (st != SC_OK) return st;
+  g.has_init = has_initial_state;
+  g.nq = q_len;
+  return from_hip(sc::launch_gdn_update(g, (hipStream_t)stream));
+}
+
+sc_status sc_gdn_update_spec(const sc_gdn_desc* desc, const void* q, const void* k,
+                             const void* v, const void* a, const void* b, const float* A_log,
+                             const float* dt_bias, void* out, float* state_pool,
+                             int32_t num_slots, const int32_t* state_indices,
+                             const int32_t* num_accepted_tokens, int32_t batch, int32_t q_len,
+                             void* stream) {
+  if (!desc) return SC_ERR_NULL_ARG;
+  sc_status st = check_gdn_desc(desc);
+  if (st != SC_OK) return st;
+  if (batch < 0 || q_len < 0 || num_slots < 0) return SC_ERR_INVALID_ARG;
+  // a row of slots per request, one for each draft
+  if (desc->state_indices_stride < q_len) return SC_ERR_INVALID_ARG;
+  if (batch == 0 || q_len == 0) return SC_OK;
+  if ((int64_t)batch * q_len > 0x7FFFFFFFLL) return SC_ERR_UNSUPPORTED;
+  if (!num_accepted_tokens) return SC_ERR_NULL_ARG;
+  sc::GdnArgs g;
+  st = gdn_args(desc, q, k, v, a, b, A_log, dt_bias, out, state_pool, num_slots, state_indices,
+                batch, &g);
+  if (st != SC_OK) return st;
+  g.num_acc = num_accepted_tokens;
+  g.nq = q_len;
+  return from_hip(sc::launch_gdn_update(g, (hipStream_t)stream));
 }
 
 }  // extern "C"
