@@ -365,6 +365,97 @@ sc_status sc_gdn_update_spec(const sc_gdn_desc* desc, const void* q, const void*
                              const int32_t* num_accepted_tokens, int32_t batch, int32_t q_len,
                              void* stream);
 
+/* A paged cache of keys or values: (num_blocks, block_size, num_kv_heads,
+ * head_dim) bf16 with a unit stride in head_dim; element strides of the other
+ * three dimensions (so heads before tokens, or keys and values in one
+ * allocation, are the caller's choice). Token s of the cache is row
+ * s % block_size of block s / block_size. */
+typedef struct {
+  void* data;              /* (device) */
+  int64_t block_stride, token_stride, head_stride;
+} sc_paged_cache;
+
+/* Norms of query and key heads, position rotation and cache write (ZAYA page:
+ * what its attention does with the [query | key | value] rows of
+ * ZayaCCA.project before it attends). Per head x of head_dim values:
+ *   x^ = weight * x / sqrt(mean(x^2) + eps)           (weight NULL: 1)
+ *   pair i of the first rotary_dim values turns by the table's angle i:
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin), the pair being values
+ *   (i, i + rotary_dim/2), or (2i, 2i + 1) with interleaved = 1
+ * in fp32 with one rounding at the store. Values are copied. */
+typedef struct {
+  int32_t num_q_heads, num_kv_heads;
+  int32_t head_dim;        /* 64, 128 or 256 (SC_ERR_UNSUPPORTED otherwise) */
+  int32_t rotary_dim;      /* 0 (no rotation) .. head_dim, a multiple of 8 */
+  int32_t interleaved;     /* 0 or 1 */
+  int32_t dtype;           /* SC_DTYPE_BF16 */
+  int32_t table_dtype;     /* sc_dtype of cos_sin */
+  float eps;               /* >= 0 */
+  int32_t block_size, num_blocks;                   /* of the caches */
+  int64_t q_row_stride, k_row_stride, v_row_stride; /* elements */
+  int64_t q_out_row_stride, k_out_row_stride, table_row_stride;
+  int64_t max_position;    /* rows of cos_sin */
+} sc_qk_norm_desc;
+
+/*   q, k, v   (device) (T, heads * head_dim) rows, 8-byte aligned, strides a
+ *             multiple of 4 (e.g. column blocks of the CCA output rows)
+ *   q_out     (device) (T, num_q_heads * head_dim); k_out the same for keys, or
+ *             NULL; q_out == q and k_out == k (the same stride) work in place,
+ *             other overlaps are not allowed
+ *   q_weight, k_weight (device) bf16 (head_dim) or NULL
+ *   cos_sin   (device) (max_position, rotary_dim): cos of the rotary_dim/2
+ *             angles, then sin; NULL with rotary_dim = 0
+ *   positions (device) int64 (T), clamped to [0, max_position); NULL with
+ *             rotary_dim = 0
+ *   slots     (device) int64 (T): the cache row of each token; a row outside
+ *             the cache (-1: padding) is not written. Required with a cache.
+ *   k_cache, v_cache (host) NULL or a cache, both or neither; v may be NULL
+ *             without them. Rows must be distinct within one call. */
+sc_status sc_qk_norm_rope(const sc_qk_norm_desc* desc, const void* q, const void* k,
+                          const void* v, void* q_out, void* k_out, const void* q_weight,
+                          const void* k_weight, const void* cos_sin, const int64_t* positions,
+                          const int64_t* slots, const sc_paged_cache* k_cache,
+                          const sc_paged_cache* v_cache, int64_t num_tokens, void* stream);
+
+/* Attention of the newest tokens over a paged cache (the attention that reads
+ * what sc_qk_norm_rope wrote). `batch` requests of exactly q_len new tokens,
+ * request r owning rows [r*q_len, (r+1)*q_len) of q and out; its cache holds
+ * seq_lens[r] tokens, the new ones last, so new token j sees positions
+ * [0, seq_lens[r] - q_len + j]. Query head h reads key/value head
+ * h / (num_q_heads / num_kv_heads).
+ *   out = sum_t softmax_t(scale q.k_t) v_t;  a row that sees nothing: zeros
+ * Scores, weights and sums are fp32. */
+typedef struct {
+  int32_t num_q_heads, num_kv_heads;
+  int32_t head_dim;        /* 64, 128 or 256 (SC_ERR_UNSUPPORTED otherwise) */
+  int32_t dtype;           /* SC_DTYPE_BF16 */
+  int32_t block_size;      /* a multiple of 16 (SC_ERR_UNSUPPORTED otherwise) */
+  int32_t num_blocks;
+  float scale;             /* finite */
+  int64_t q_row_stride, out_row_stride;   /* elements, multiples of 8 and 4 */
+  int64_t block_table_row_stride;         /* >= max_blocks */
+} sc_paged_attn_desc;
+
+/* Bytes of workspace for these sizes on the current device (host only; 0 when
+ * the cache's length is not split). */
+sc_status sc_paged_attn_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
+                                        int32_t q_len, int32_t max_seq_len, int64_t* bytes);
+
+/*   block_table (device) int32 (batch, max_blocks): block of each block_size
+ *               tokens; entries behind a request's last token are not read; a
+ *               block outside the cache holds no visible token
+ *   seq_lens    (device) int32 (batch), clamped to [0, max_seq_len]
+ *   max_seq_len (host) <= max_blocks * block_size; the split follows from it
+ *   workspace   (device) 16-byte aligned, or NULL if none is needed; scratch:
+ *               calls that may run at once need one each
+ * Cache pointers 16-byte aligned, strides a multiple of 8. */
+sc_status sc_paged_attn_decode(const sc_paged_attn_desc* desc, const void* q, void* out,
+                               const sc_paged_cache* k_cache, const sc_paged_cache* v_cache,
+                               const int32_t* block_table, int32_t max_blocks,
+                               const int32_t* seq_lens, int32_t batch, int32_t q_len,
+                               int32_t max_seq_len, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
 /* Checks the device-side preconditions the calls above document but cannot
  * check without a host sync (a debugging and test aid, not for the hot path):
  * waits for `stream`, copies the metadata to the host and returns

@@ -30,6 +30,7 @@ EXPORTS = ("sc_conv_prefill_varlen", "sc_conv_update", "sc_conv_update_spec",
            "sc_conv_update_spec_varlen", "sc_validate_metadata", "sc_state_gather",
            "sc_state_scatter", "sc_cca_qk_conv", "sc_gdn_workspace_bytes",
            "sc_gdn_prefill_varlen", "sc_gdn_update", "sc_gdn_update_spec",
+           "sc_qk_norm_rope", "sc_paged_attn_workspace_bytes", "sc_paged_attn_decode",
            "sc_status_string", "sc_abi_version")
 
 
@@ -78,6 +79,31 @@ class sc_gdn_desc(ctypes.Structure):
                 ("v_row_stride", ctypes.c_int64), ("a_row_stride", ctypes.c_int64),
                 ("b_row_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
                 ("state_indices_stride", ctypes.c_int64)]
+
+
+class sc_paged_cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("block_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class sc_qk_norm_desc(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("table_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("q_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+                ("v_row_stride", ctypes.c_int64), ("q_out_row_stride", ctypes.c_int64),
+                ("k_out_row_stride", ctypes.c_int64), ("table_row_stride", ctypes.c_int64),
+                ("max_position", ctypes.c_int64)]
+
+
+class sc_paged_attn_desc(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q_row_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("block_table_row_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -130,6 +156,15 @@ def lib():
         L.sc_gdn_update.argtypes = [G, P, P, P, P, P, P, P, P, P, I32, P, P, I32, I32, P]
         L.sc_gdn_update_spec.restype = I32
         L.sc_gdn_update_spec.argtypes = [G, P, P, P, P, P, P, P, P, P, I32, P, P, I32, I32, P]
+        PC = ctypes.POINTER(sc_paged_cache)
+        PA = ctypes.POINTER(sc_paged_attn_desc)
+        L.sc_qk_norm_rope.restype = I32
+        L.sc_qk_norm_rope.argtypes = [ctypes.POINTER(sc_qk_norm_desc), P, P, P, P, P, P, P, P, P,
+                                      P, PC, PC, I64, P]
+        L.sc_paged_attn_workspace_bytes.restype = I32
+        L.sc_paged_attn_workspace_bytes.argtypes = [PA, I32, I32, I32, ctypes.POINTER(I64)]
+        L.sc_paged_attn_decode.restype = I32
+        L.sc_paged_attn_decode.argtypes = [PA, P, P, PC, PC, P, I32, P, I32, I32, I32, P, I64, P]
         L.sc_status_string.restype = ctypes.c_char_p
         L.sc_status_string.argtypes = [I32]
         L.sc_abi_version.restype = I32
@@ -690,3 +725,155 @@ def sc_gdn_update_spec(query, key, value, a, b, A_log, dt_bias, out, state_pool,
         _ptr(dt_bias), _ptr(out), _ptr(state_pool), state_pool.shape[0], _ptr(state_indices),
         _ptr(num_accepted_tokens), batch, q, _stream(stream, query))
     _check("sc_gdn_update_spec", st)
+
+
+def _paged(cache, name, nkv, hd, like):
+    """Descriptor of a (num_blocks, block_size, nkv, hd) cache tensor."""
+    if cache.dim() != 4 or tuple(cache.shape[2:]) != (nkv, hd) or cache.dtype != like.dtype:
+        raise ValueError(f"{name}: expected (num_blocks, block_size, {nkv}, {hd}) of {like.dtype}")
+    if cache.stride(3) != 1:
+        raise ValueError(f"{name}: expected a unit stride in head_dim")
+    # the stride of a dimension of one entry is never used
+    st = [cache.stride(i) if cache.shape[i] > 1 else 0 for i in range(3)]
+    return sc_paged_cache(data=_ptr(cache), block_stride=st[0], token_stride=st[1],
+                          head_stride=st[2])
+
+
+def _int64s(t, name, n):
+    torch = _torch()
+    if t.dtype != torch.int64 or not t.is_contiguous() or t.dim() != 1 or t.shape[0] < n:
+        raise ValueError(f"{name}: expected a contiguous int64 tensor of {n} entries")
+    return _ptr(t)
+
+
+def sc_qk_norm_rope(query, key, value, q_out, k_out, q_weight, k_weight, cos_sin, positions,
+                    slots, k_cache, v_cache, *, head_dim: int, eps: float = 1e-6,
+                    interleaved: bool = False, stream=None):
+    """Norms of the query and key heads, position rotation, and the write of keys
+    and values into a paged cache.
+
+    query (T, nq * head_dim), key, value (T, nkv * head_dim) bf16 rows (column
+    blocks of sc_cca_qk_conv's output rows will do); q_out like query; k_out
+    like key or None; q_out = query or k_out = key work in place. q_weight,
+    k_weight: (head_dim) bf16 or None. cos_sin: (positions, rotary_dim) fp32 or
+    bf16, cos then sin, or None (no rotation). positions, slots: int64 (T); slot
+    -1 is not written. k_cache, v_cache: (num_blocks, block_size, nkv,
+    head_dim), or None for both (value and slots are then not read).
+    """
+    T = query.shape[0]
+    if head_dim < 1 or query.shape[1] % head_dim or key.shape[1] % head_dim:
+        raise ValueError(f"query, key: expected rows of heads of {head_dim} values")
+    if (k_cache is None) != (v_cache is None):
+        raise ValueError("k_cache, v_cache: expected both or neither")
+    nq, nkv = query.shape[1] // head_dim, key.shape[1] // head_dim
+    for name, t, w in (("key", key, nkv), ("value", value, nkv), ("q_out", q_out, nq),
+                       ("k_out", k_out, nkv)):
+        if t is None and (name == "k_out" or (name == "value" and k_cache is None)):
+            continue
+        if t.dim() != 2 or t.shape[1] != w * head_dim or t.shape[0] < T or t.dtype != query.dtype:
+            raise ValueError(f"{name}: expected ({T}, {w * head_dim}) of {query.dtype}")
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None and (t.numel() != head_dim or not t.is_contiguous() or
+                              t.dtype != query.dtype):
+            raise ValueError(f"{name}: expected a contiguous tensor of {head_dim} entries of "
+                             f"{query.dtype}")
+    kc = vc = None
+    if k_cache is not None:
+        kc = _paged(k_cache, "k_cache", nkv, head_dim, query)
+        vc = _paged(v_cache, "v_cache", nkv, head_dim, query)
+        if k_cache.shape[:2] != v_cache.shape[:2]:
+            raise ValueError("k_cache, v_cache: expected the same blocks")
+    rows = lambda t, n: 0 if t is None else _rows(t, n)
+    desc = sc_qk_norm_desc(
+        num_q_heads=nq, num_kv_heads=nkv, head_dim=head_dim,
+        rotary_dim=0 if cos_sin is None else cos_sin.shape[1],
+        interleaved=1 if interleaved else 0, dtype=_dtype_code(query),
+        table_dtype=SC_DTYPE_F32 if cos_sin is None else _dtype_code(cos_sin), eps=eps,
+        block_size=1 if kc is None else k_cache.shape[1],
+        num_blocks=0 if kc is None else k_cache.shape[0], q_row_stride=_rows(query, "query"),
+        k_row_stride=_rows(key, "key"), v_row_stride=rows(value, "value"),
+        q_out_row_stride=_rows(q_out, "q_out"), k_out_row_stride=rows(k_out, "k_out"),
+        table_row_stride=rows(cos_sin, "cos_sin"),
+        max_position=0 if cos_sin is None else cos_sin.shape[0])
+    st = lib().sc_qk_norm_rope(
+        ctypes.byref(desc), _ptr(query), _ptr(key), None if kc is None else _ptr(value),
+        _ptr(q_out), _ptr(k_out), _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
+        None if cos_sin is None else _int64s(positions, "positions", T),
+        None if kc is None else _int64s(slots, "slots", T),
+        None if kc is None else ctypes.byref(kc), None if vc is None else ctypes.byref(vc), T,
+        _stream(stream, query))
+    _check("sc_qk_norm_rope", st)
+
+
+def _attn_desc(query, out, k_cache, block_table, q, scale):
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
+    blocks, block_size, nkv, hd = k_cache.shape
+    if hd < 1 or query.dim() != 2 or query.shape[1] % hd or query.shape[1] == 0:
+        raise ValueError(f"query: expected rows of heads of {hd} values")
+    if q < 1 or query.shape[0] % q:
+        raise ValueError("rows must be a multiple of q >= 1")
+    if out.dim() != 2 or out.shape[1] != query.shape[1] or out.shape[0] < query.shape[0] or \
+            out.dtype != query.dtype:
+        raise ValueError("out: expected the shape and dtype of query")
+    if block_table.dim() != 2 or block_table.dtype != _torch().int32 or \
+            (block_table.shape[1] > 1 and block_table.numel() and block_table.stride(1) != 1):
+        raise ValueError("block_table: expected int32 (batch, max_blocks) with adjacent entries")
+    return sc_paged_attn_desc(
+        num_q_heads=query.shape[1] // hd, num_kv_heads=nkv, head_dim=hd,
+        dtype=_dtype_code(query), block_size=block_size, num_blocks=blocks,
+        scale=hd ** -0.5 if scale is None else scale, q_row_stride=_rows(query, "query"),
+        out_row_stride=_rows(out, "out"),
+        block_table_row_stride=block_table.stride(0) if block_table.shape[0] > 1
+        else max(block_table.shape[1], 1))
+
+
+def _attn_need(desc, batch, q, max_seq_len) -> int:
+    n = ctypes.c_int64(0)
+    _check("sc_paged_attn_workspace_bytes", lib().sc_paged_attn_workspace_bytes(
+        ctypes.byref(desc), batch, q, max_seq_len, ctypes.byref(n)))
+    return n.value
+
+
+def sc_paged_attn_workspace_bytes(batch: int, *, q: int = 1, max_seq_len: int, num_q_heads: int,
+                                  num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace that sc_paged_attn_decode needs for these sizes on the
+    current device (0 where the cache's length is not split)."""
+    w = num_q_heads * head_dim
+    return _attn_need(sc_paged_attn_desc(
+        num_q_heads=num_q_heads, num_kv_heads=num_kv_heads, head_dim=head_dim,
+        dtype=SC_DTYPE_BF16, block_size=16, num_blocks=1, scale=1.0, q_row_stride=w,
+        out_row_stride=w, block_table_row_stride=1), batch, q, max_seq_len)
+
+
+def sc_paged_attn_decode(query, out, k_cache, v_cache, block_table, seq_lens, *,
+                         max_seq_len: int, q: int = 1, scale: Optional[float] = None,
+                         workspace=None, stream=None):
+    """Attention of each request's `q` newest tokens over its paged cache.
+
+    query, out: (B * q, nq * hd) bf16, request r owning rows [r*q, (r+1)*q);
+    k_cache, v_cache: (num_blocks, block_size, nkv, hd), block_size a multiple
+    of 16; block_table int32 (B, max_blocks); seq_lens int32 (B), the tokens in
+    the cache with the new ones last; max_seq_len bounds them. scale defaults
+    to hd ** -0.5. workspace: None, or a tensor of
+    sc_paged_attn_workspace_bytes bytes to reuse (one for each call that may
+    run at the same time).
+    """
+    torch = _torch()
+    desc = _attn_desc(query, out, k_cache, block_table, q, scale)
+    batch = query.shape[0] // q
+    kc = _paged(k_cache, "k_cache", desc.num_kv_heads, desc.head_dim, query)
+    vc = _paged(v_cache, "v_cache", desc.num_kv_heads, desc.head_dim, query)
+    if k_cache.shape[:2] != v_cache.shape[:2]:
+        raise ValueError("k_cache, v_cache: expected the same blocks")
+    if seq_lens.dtype != torch.int32 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens: expected a contiguous int32 tensor")
+    _covers(batch, block_table=block_table, seq_lens=seq_lens)
+    raw = _stream(stream, query)
+    need = _attn_need(desc, batch, q, max_seq_len)
+    workspace = _workspace(workspace, need, query, stream)
+    st = lib().sc_paged_attn_decode(
+        ctypes.byref(desc), _ptr(query), _ptr(out), ctypes.byref(kc), ctypes.byref(vc),
+        _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, q, max_seq_len,
+        _ptr(workspace), _nbytes(workspace), raw)
+    _check("sc_paged_attn_decode", st)

@@ -10,12 +10,14 @@
 
 #include "statefulconv.h"
 #include "kernels.hpp"
+#include "attn.hpp"
 #include "cca.hpp"
 #include "gdn.hpp"
 
 namespace {
 
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool al8(const void* p) { return ((uintptr_t)p & 7u) == 0; }
 
 // Descriptor checks shared by the depthwise entry points. The state-capacity
 // rule follows the PLE layer's _short_conv (cache narrower than the window
@@ -168,6 +170,65 @@ sc_status gdn_args(const sc_gdn_desc* d, const void* q, const void* k, const voi
   g->gate_f32 = d->gate_dtype == SC_DTYPE_F32;
   g->num_slots = num_slots;
   g->batch = batch;
+  return SC_OK;
+}
+
+// Head counts and sizes shared by the norm and attention calls.
+sc_status check_heads(int32_t dtype, int32_t nq, int32_t nkv, int32_t hd) {
+  if (dtype != SC_DTYPE_BF16) return SC_ERR_DTYPE;
+  if (nq < 1 || nkv < 1 || nq % nkv != 0 || hd < 1) return SC_ERR_INVALID_ARG;
+  if (hd != 64 && hd != 128 && hd != 256) return SC_ERR_UNSUPPORTED;
+  if (nq > (1 << 20)) return SC_ERR_UNSUPPORTED;
+  return SC_OK;
+}
+
+sc_status check_paged(const sc_paged_cache* c, int32_t block_size, int64_t multiple,
+                      sc::PagedCache* out) {
+  if (!c->data) return SC_ERR_NULL_ARG;
+  if (c->block_stride < 0 || c->token_stride < 0 || c->head_stride < 0 || block_size < 1)
+    return SC_ERR_INVALID_ARG;
+  if (c->block_stride % multiple != 0 || c->token_stride % multiple != 0 ||
+      c->head_stride % multiple != 0 || ((uintptr_t)c->data & (multiple * 2 - 1)) != 0)
+    return SC_ERR_UNSUPPORTED;
+  *out = sc::PagedCache{c->data, c->block_stride, c->token_stride, c->head_stride};
+  return SC_OK;
+}
+
+sc_status check_attn_desc(const sc_paged_attn_desc* d) {
+  const sc_status st = check_heads(d->dtype, d->num_q_heads, d->num_kv_heads, d->head_dim);
+  if (st != SC_OK) return st;
+  const int64_t w = (int64_t)d->num_q_heads * d->head_dim;
+  if (d->block_size < 1 || d->num_blocks < 0 || !std::isfinite(d->scale) ||
+      d->q_row_stride < w || d->out_row_stride < w || d->block_table_row_stride < 1)
+    return SC_ERR_INVALID_ARG;
+  if (d->block_size % 16 != 0 || d->q_row_stride % 8 != 0 || d->out_row_stride % 4 != 0)
+    return SC_ERR_UNSUPPORTED;
+  return SC_OK;
+}
+
+// Sizes of an attention call and its split; workspace bytes through *need.
+sc_status attn_sizes(const sc_paged_attn_desc* d, int32_t batch, int32_t q_len,
+                     int32_t max_seq_len, sc::PagedAttnArgs* a, int64_t* need) {
+  if (batch < 0 || q_len < 0 || max_seq_len < 0) return SC_ERR_INVALID_ARG;
+  // rows, row groups and splits are counted with 32 bits
+  if ((int64_t)batch * q_len * d->num_q_heads > 0x7FFFFFFFLL || max_seq_len > 0x7FFF0000)
+    return SC_ERR_UNSUPPORTED;
+  *a = sc::PagedAttnArgs{};
+  *need = 0;
+  if (batch == 0 || q_len == 0) return SC_OK;
+  a->q_rs = d->q_row_stride;
+  a->out_rs = d->out_row_stride;
+  a->table_rs = d->block_table_row_stride;
+  a->scale = d->scale;
+  a->batch = batch;
+  a->nq_tok = q_len;
+  a->nq = d->num_q_heads;
+  a->nkv = d->num_kv_heads;
+  a->hd = d->head_dim;
+  a->block_size = d->block_size;
+  a->num_blocks = d->num_blocks;
+  a->max_len = max_seq_len;
+  *need = sc::plan_paged_attn(a);
   return SC_OK;
 }
 
@@ -589,6 +650,121 @@ sc_status sc_gdn_update_spec(const sc_gdn_desc* desc, const void* q, const void*
   g.num_acc = num_accepted_tokens;
   g.nq = q_len;
   return from_hip(sc::launch_gdn_update(g, (hipStream_t)stream));
+}
+
+sc_status sc_qk_norm_rope(const sc_qk_norm_desc* desc, const void* q, const void* k,
+                          const void* v, void* q_out, void* k_out, const void* q_weight,
+                          const void* k_weight, const void* cos_sin, const int64_t* positions,
+                          const int64_t* slots, const sc_paged_cache* k_cache,
+                          const sc_paged_cache* v_cache, int64_t num_tokens, void* stream) {
+  if (!desc) return SC_ERR_NULL_ARG;
+  const int nq = desc->num_q_heads, nkv = desc->num_kv_heads, hd = desc->head_dim;
+  sc_status st = check_heads(desc->dtype, nq, nkv, hd);
+  if (st != SC_OK) return st;
+  if (desc->table_dtype != SC_DTYPE_F32 && desc->table_dtype != SC_DTYPE_BF16)
+    return SC_ERR_DTYPE;
+  const int rot = desc->rotary_dim;
+  if (rot < 0 || rot > hd || (desc->interleaved != 0 && desc->interleaved != 1) ||
+      !(desc->eps >= 0) || num_tokens < 0 || desc->num_blocks < 0)
+    return SC_ERR_INVALID_ARG;
+  if (rot % 8 != 0) return SC_ERR_UNSUPPORTED;
+  const int64_t qw = (int64_t)nq * hd, kw = (int64_t)nkv * hd;
+  if (desc->q_row_stride < qw || desc->k_row_stride < kw || desc->q_out_row_stride < qw ||
+      (k_out && desc->k_out_row_stride < kw) || (k_cache && desc->v_row_stride < kw) ||
+      (rot > 0 && (desc->table_row_stride < rot || desc->max_position < 1)))
+    return SC_ERR_INVALID_ARG;
+  if (!k_cache != !v_cache) return SC_ERR_NULL_ARG;
+  if (num_tokens == 0) return SC_OK;
+  if (!q || !k || !q_out || (rot > 0 && (!cos_sin || !positions)) || (k_cache && (!v || !slots)))
+    return SC_ERR_NULL_ARG;
+  // in place only on the same rows: a lane then rewrites what it alone has read
+  if ((q_out == q && desc->q_out_row_stride != desc->q_row_stride) ||
+      (k_out && k_out == k && desc->k_out_row_stride != desc->k_row_stride) || q_out == k ||
+      q_out == k_out || k_out == q)
+    return SC_ERR_INVALID_ARG;
+  sc::QkNormArgs a{};
+  if (k_cache) {
+    if ((st = check_paged(k_cache, desc->block_size, 4, &a.kc)) != SC_OK) return st;
+    if ((st = check_paged(v_cache, desc->block_size, 4, &a.vc)) != SC_OK) return st;
+  }
+  if (!al8(q) || !al8(k) || !al8(q_out) || !al8(k_out) || !al8(q_weight) || !al8(k_weight) ||
+      (k_cache && (!al8(v) || desc->v_row_stride % 4 != 0)) || desc->q_row_stride % 4 != 0 ||
+      desc->k_row_stride % 4 != 0 || desc->q_out_row_stride % 4 != 0 ||
+      (k_out && desc->k_out_row_stride % 4 != 0))
+    return SC_ERR_UNSUPPORTED;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.q_w = q_weight;
+  a.k_w = k_weight;
+  a.table = cos_sin;
+  a.positions = positions;
+  a.slots = k_cache ? slots : nullptr;
+  a.q_rs = desc->q_row_stride;
+  a.k_rs = desc->k_row_stride;
+  a.v_rs = desc->v_row_stride;
+  a.qo_rs = desc->q_out_row_stride;
+  a.ko_rs = desc->k_out_row_stride;
+  a.table_rs = desc->table_row_stride;
+  a.max_pos = desc->max_position;
+  a.num_tokens = num_tokens;
+  a.eps = desc->eps;
+  a.nq = nq;
+  a.nkv = nkv;
+  a.hd = hd;
+  a.rot = rot;
+  a.interleaved = desc->interleaved;
+  a.table_f32 = desc->table_dtype == SC_DTYPE_F32;
+  a.block_size = desc->block_size;
+  a.num_blocks = desc->num_blocks;
+  return from_hip(sc::launch_qk_norm(a, (hipStream_t)stream));
+}
+
+sc_status sc_paged_attn_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
+                                        int32_t q_len, int32_t max_seq_len, int64_t* bytes) {
+  if (!desc || !bytes) return SC_ERR_NULL_ARG;
+  sc_status st = check_attn_desc(desc);
+  if (st != SC_OK) return st;
+  sc::PagedAttnArgs a;
+  return attn_sizes(desc, batch, q_len, max_seq_len, &a, bytes);
+}
+
+sc_status sc_paged_attn_decode(const sc_paged_attn_desc* desc, const void* q, void* out,
+                               const sc_paged_cache* k_cache, const sc_paged_cache* v_cache,
+                               const int32_t* block_table, int32_t max_blocks,
+                               const int32_t* seq_lens, int32_t batch, int32_t q_len,
+                               int32_t max_seq_len, void* workspace, int64_t workspace_bytes,
+                               void* stream) {
+  if (!desc) return SC_ERR_NULL_ARG;
+  sc_status st = check_attn_desc(desc);
+  if (st != SC_OK) return st;
+  sc::PagedAttnArgs a;
+  int64_t need = 0;
+  if ((st = attn_sizes(desc, batch, q_len, max_seq_len, &a, &need)) != SC_OK) return st;
+  if (max_blocks < 0 || workspace_bytes < 0 || desc->block_table_row_stride < max_blocks ||
+      max_seq_len > (int64_t)max_blocks * desc->block_size)
+    return SC_ERR_INVALID_ARG;
+  if (batch == 0 || q_len == 0) return SC_OK;
+  // no cached token anywhere: the rows are zeros, and no table is needed
+  if (!q || !out || !seq_lens || (max_seq_len > 0 && (!block_table || !k_cache || !v_cache)) ||
+      (need > 0 && !workspace))
+    return SC_ERR_NULL_ARG;
+  if (out == q || workspace_bytes < need || (need > 0 && !al16(workspace)))
+    return SC_ERR_INVALID_ARG;
+  if (max_seq_len > 0) {
+    if ((st = check_paged(k_cache, desc->block_size, 8, &a.kc)) != SC_OK) return st;
+    if ((st = check_paged(v_cache, desc->block_size, 8, &a.vc)) != SC_OK) return st;
+    if (desc->num_blocks < 1) return SC_ERR_INVALID_ARG;
+  }
+  if (!al16(q) || !al8(out)) return SC_ERR_UNSUPPORTED;
+  a.q = q;
+  a.out = out;
+  a.table = block_table;
+  a.lens = seq_lens;
+  a.ws = (float*)workspace;
+  return from_hip(sc::launch_paged_attn(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,363 @@
+// Attention of one or a few new tokens per request over a paged cache.
+//
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t - max)
+//
+// over the positions a token sees. The bytes of the cache bound it: keys and
+// values are read once from HBM straight into registers, as MFMA operands.
+//
+// A group of up to 16 rows (the query heads of one key/value head, times the
+// request's new tokens) shares each key: scores of 16 cached tokens x 16 rows
+// are one 16x16x32 bf16 product per 32 values of a head, with the keys as the
+// left operand as they lie in the cache. A score tile then has row n = lane %
+// 16 and tokens 4 (lane / 16) + i in register i, which is how the fp32
+// 16x16x4 product wants its left operand when product i sums over tokens
+// 4 g + i, g = 0..3. So p goes from the softmax to the second product in its
+// registers, in fp32, and the values are read 16 lanes to a token's row.
+//
+// Work split: a workgroup has one (request, key/value head, row group, split of
+// the cache's length); its four waves take 16-token tiles in turn, each with a
+// running maximum and sum, and join in LDS at the end. With more than one split
+// the parts go to the workspace and attn_join adds them.
+#include "attn.hpp"
+#include "common.hpp"
+
+#include <algorithm>
+
+namespace sc {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+namespace {
+
+constexpr int kTile = 16;        // cached tokens per tile
+constexpr int kRows = 16;        // query rows per workgroup
+constexpr int kMaxSplits = 64;
+constexpr float kNone = -3.0e38f;   // running maximum before any token
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Whether one of four bf16 values is infinite or NaN.
+__device__ __forceinline__ bool any_special(uint2 w) {
+  auto special = [](uint32_t x) {
+    return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+  };
+  return special(w.x) || special(w.y);
+}
+
+}  // namespace
+
+// Workspace: for each (query row, split) the maximum, the sum and hd values.
+template <int HD>
+__global__ __launch_bounds__(kBlock) void attn_split(PagedAttnArgs a) {
+  constexpr int KS = HD / 32;               // score products per tile
+  constexpr int VPL = HD / 16;              // values of a token's row per lane
+  constexpr int VW = VPL / 4;               // ... in 8-byte words
+  __shared__ __align__(16) float Ol[3][kRows * HD];
+  __shared__ float ml[3][kRows], ll[3][kRows];
+
+  const int group = a.nq / a.nkv, rows = group * a.nq_tok;
+  const int row_groups = (rows + kRows - 1) / kRows;
+  unsigned id = blockIdx.x;
+  const int kvh = (int)(id % (unsigned)a.nkv);
+  id /= (unsigned)a.nkv;
+  const int split = (int)(id % (unsigned)a.splits);
+  id /= (unsigned)a.splits;
+  const int rg = (int)(id % (unsigned)row_groups);
+  const int r = (int)(id / (unsigned)row_groups);
+
+  const int lane = (int)(threadIdx.x & 63);
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int l16 = lane & 15, lg = lane >> 4;
+  const int len = min(max(a.lens[r], 0), a.max_len);
+  const int t_lo = split * a.split_len, t_hi = min(len, t_lo + a.split_len);
+  if (split > 0 && t_lo >= len) return;      // the join does not read such a split
+
+  // this lane's query row: head kvh * group + g of new token j
+  const int row = rg * kRows + l16;
+  const bool row_ok = row < rows;
+  const int j = row_ok ? row / group : 0, g = row_ok ? row - j * group : 0;
+  const int64_t q_row = (int64_t)r * a.nq_tok + j;
+  const int head = kvh * group + g;
+  const int limit = row_ok ? len - a.nq_tok + j : -1;   // last visible position
+  u32x4 qf[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    qf[s] = u32x4{0, 0, 0, 0};
+    if (row_ok)
+      qf[s] = ld16((const uint16_t*)a.q + q_row * a.q_rs + (int64_t)head * HD + s * 32 + lg * 8);
+  }
+
+  float m = kNone, l = 0.f;
+  f32x4 O[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) O[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const float c = a.scale * 1.4426950408889634f;
+  const int32_t* const table = a.table + (int64_t)r * a.table_rs;
+  const uint16_t* const kbase = (const uint16_t*)a.kc.p + (int64_t)kvh * a.kc.head_s;
+  const uint16_t* const vbase = (const uint16_t*)a.vc.p + (int64_t)kvh * a.vc.head_s;
+
+  struct Tile {
+    u32x4 k[KS];
+    uint2 v[4][VW];
+    bool ok;
+  };
+  // A tile lies in one page (pages are multiples of 16 tokens). A page id
+  // outside the cache makes the tile invisible.
+  auto load = [&](Tile& x, int t0) {
+    const int b = t0 / a.block_size;
+    const int page = table[b];
+    x.ok = page >= 0 && page < a.num_blocks;
+    const int64_t pg = x.ok ? page : 0;
+    const int in = t0 - b * a.block_size;
+    const uint16_t* kp = kbase + pg * a.kc.block_s + (int64_t)(in + l16) * a.kc.token_s + lg * 8;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) x.k[s] = ld16(kp + s * 32);
+    const uint16_t* vp = vbase + pg * a.vc.block_s + (int64_t)(in + lg * 4) * a.vc.token_s + l16 * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int u = 0; u < VW; ++u) x.v[i][u] = *(const uint2*)(vp + (int64_t)i * a.vc.token_s + u * 64);
+  };
+  Tile cur, nxt;
+  int t0 = t_lo + w * kTile;
+  if (t0 < t_hi) load(cur, t0);
+  for (; t0 < t_hi; t0 += 4 * kTile) {
+    if (t0 + 4 * kTile < t_hi) load(nxt, t0 + 4 * kTile);
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+      s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cur.k[ks]),
+                                                  __builtin_bit_cast(bf16x8, qf[ks]), s, 0, 0, 0);
+    float top = kNone;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + lg * 4 + i;
+      // positions behind the tile's last visible one hold anything, NaN included
+      s[i] = cur.ok && t <= limit && t < t_hi ? s[i] * c : -INFINITY;
+      top = fmaxf(top, s[i]);
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // the accumulators are rescaled only when some row's maximum grows
+    if (__any(top > m)) {
+      const float mn = fmaxf(m, top);
+      const float f = exp2_(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float fi = __shfl(f, lg * 4 + i);
+#pragma unroll
+        for (int d = 0; d < VPL; ++d) O[d][i] *= fi;
+      }
+    }
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = exp2_(s[i] - m);
+      l += p[i];
+    }
+    // Value rows behind the visible ones hold anything, NaN included, which a
+    // weight of 0 would not undo: they count as zeros. So do the non-finite
+    // values of a row that only the later drafts see; those are added apart.
+    uint32_t odd = 0;
+    if (a.nq_tok > 1 && t0 + kTile > len - a.nq_tok + 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bool bad = false;
+#pragma unroll
+        for (int u = 0; u < VW; ++u) bad = bad || any_special(cur.v[i][u]);
+        if (bad && t0 + lg * 4 + i > len - a.nq_tok) odd |= 1u << i;
+      }
+      if (__any(odd != 0)) {
+        for (int tt = 0; tt < kTile; ++tt) {
+          const int from = (tt >> 2) * 16, t = t0 + tt;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i != (tt & 3)) continue;
+            // a row of 16 lanes holds a token: odd if any of its lanes is
+            if (!(__ballot((odd >> i) & 1) >> from & 0xFFFF)) continue;
+#pragma unroll
+            for (int ii = 0; ii < 4; ++ii) {
+              const float pw = __shfl(p[i], from + lg * 4 + ii);
+              const bool sees = __shfl(limit, lg * 4 + ii) >= t && cur.ok && t < t_hi;
+#pragma unroll
+              for (int u = 0; u < VW; ++u) {
+                const uint32_t x0 = __shfl((int)cur.v[i][u].x, from + l16);
+                const uint32_t x1 = __shfl((int)cur.v[i][u].y, from + l16);
+                if (sees) {
+                  O[u * 4 + 0][ii] += pw * __uint_as_float(x0 << 16);
+                  O[u * 4 + 1][ii] += pw * __uint_as_float(x0 & 0xFFFF0000u);
+                  O[u * 4 + 2][ii] += pw * __uint_as_float(x1 << 16);
+                  O[u * 4 + 3][ii] += pw * __uint_as_float(x1 & 0xFFFF0000u);
+                }
+              }
+            }
+            if (lg == tt >> 2) odd |= 16u << i;      // the whole row was added
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool live = cur.ok && t0 + lg * 4 + i < t_hi && !((odd >> (4 + i)) & 1);
+#pragma unroll
+      for (int u = 0; u < VW; ++u) {
+        const uint32_t x0 = live ? cur.v[i][u].x : 0u, x1 = live ? cur.v[i][u].y : 0u;
+        O[u * 4 + 0] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], __uint_as_float(x0 << 16), O[u * 4 + 0], 0, 0, 0);
+        O[u * 4 + 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], __uint_as_float(x0 & 0xFFFF0000u), O[u * 4 + 1], 0, 0, 0);
+        O[u * 4 + 2] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], __uint_as_float(x1 << 16), O[u * 4 + 2], 0, 0, 0);
+        O[u * 4 + 3] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], __uint_as_float(x1 & 0xFFFF0000u), O[u * 4 + 3], 0, 0, 0);
+      }
+    }
+    cur = nxt;
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  // join the four waves: wave 0 takes in the others' parts. O[d] of a lane is
+  // value u*64 + l16*4 + e (d = 4u + e) of rows 4 lg + i.
+  if (w > 0) {
+    if (lg == 0) {
+      ml[w - 1][l16] = m;
+      ll[w - 1][l16] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int u = 0; u < VW; ++u)
+        *(f32x4*)&Ol[w - 1][(lg * 4 + i) * HD + u * 64 + l16 * 4] =
+            f32x4{O[u * 4][i], O[u * 4 + 1][i], O[u * 4 + 2][i], O[u * 4 + 3][i]};
+  }
+  __syncthreads();
+  if (w > 0) return;
+  float mt = m;
+#pragma unroll
+  for (int x = 0; x < 3; ++x) mt = fmaxf(mt, ml[x][l16]);
+  const float f0 = exp2_(m - mt);
+  float lt = l * f0, fx[3];
+#pragma unroll
+  for (int x = 0; x < 3; ++x) {
+    fx[x] = exp2_(ml[x][l16] - mt);
+    lt += ll[x][l16] * fx[x];
+  }
+  const float inv = a.splits > 1 ? 1.f : (lt > 0.f ? 1.f / lt : 0.f);
+  const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
+  float* const wo = a.ws + n_rows * a.splits * 2;
+  const int64_t part = (q_row * a.nq + head) * a.splits + split;
+  if (a.splits > 1 && row_ok && lg == 0) {
+    a.ws[part * 2] = mt;
+    a.ws[part * 2 + 1] = lt;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int src = lg * 4 + i;             // the row held in register i
+    const float g0 = __shfl(f0, src), gi = __shfl(inv, src);
+    const float g1 = __shfl(fx[0], src), g2 = __shfl(fx[1], src), g3 = __shfl(fx[2], src);
+    const int rr = rg * kRows + src;
+    const int jj = rr / group, hh = kvh * group + rr - jj * group;
+    const int64_t qr = (int64_t)r * a.nq_tok + jj;
+#pragma unroll
+    for (int u = 0; u < VW; ++u) {
+      const int at = src * HD + u * 64 + l16 * 4;
+      const f32x4 a1 = *(const f32x4*)&Ol[0][at], a2 = *(const f32x4*)&Ol[1][at],
+                  a3 = *(const f32x4*)&Ol[2][at];
+      f32x4 y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[e] = (O[u * 4 + e][i] * g0 + a1[e] * g1 + a2[e] * g2 + a3[e] * g3) * gi;
+      if (rr < rows) {
+        if (a.splits > 1) {
+          *(f32x4*)(wo + ((qr * a.nq + hh) * a.splits + split) * HD + u * 64 + l16 * 4) = y;
+        } else {
+          f32x2 y0 = {y[0], y[1]}, y1 = {y[2], y[3]};
+          *(uint2*)((uint16_t*)a.out + qr * a.out_rs + (int64_t)hh * HD + u * 64 + l16 * 4) =
+              uint2{__builtin_bit_cast(uint32_t, __builtin_convertvector(y0, bf16x2)),
+                    __builtin_bit_cast(uint32_t, __builtin_convertvector(y1, bf16x2))};
+        }
+      }
+    }
+  }
+}
+
+// Adds the splits of a query row: a wave per row, hd/64 values a lane.
+template <int HD>
+__global__ __launch_bounds__(kBlock) void attn_join(PagedAttnArgs a) {
+  constexpr int N = HD / 64;
+  const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= n_rows) return;
+  const int lane = (int)(threadIdx.x & 63);
+  const int64_t q_row = row / a.nq;
+  const int head = (int)(row - q_row * a.nq);
+  const int r = (int)(q_row / a.nq_tok);
+  const int len = min(max(a.lens[r], 0), a.max_len);
+  const int n = max(1, min(a.splits, (len + a.split_len - 1) / a.split_len));
+  const float* ml = a.ws + row * a.splits * 2;
+  const float* part = a.ws + n_rows * a.splits * 2 + row * a.splits * HD + lane * N;
+  const float mine = lane < n ? ml[lane * 2] : kNone;
+  float mt = mine;
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) mt = fmaxf(mt, __shfl_xor(mt, d));
+  const float f = lane < n ? exp2_(mine - mt) : 0.f;
+  float lt = lane < n ? ml[lane * 2 + 1] * f : 0.f;
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) lt += __shfl_xor(lt, d);
+  float y[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) y[e] = 0.f;
+  for (int s = 0; s < n; ++s) {
+    const float fs = __shfl(f, s);
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] = fmaf(part[(int64_t)s * HD + e], fs, y[e]);
+  }
+  const float inv = lt > 0.f ? 1.f / lt : 0.f;
+  uint16_t* o = (uint16_t*)a.out + q_row * a.out_rs + (int64_t)head * HD + lane * N;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    f32x2 p = {y[e] * inv, 0.f};
+    o[e] = (uint16_t)__builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+  }
+}
+
+int64_t plan_paged_attn(PagedAttnArgs* a) {
+  const int64_t rows = (int64_t)(a->nq / a->nkv) * a->nq_tok;
+  const int64_t base = (int64_t)a->batch * a->nkv * ((rows + kRows - 1) / kRows);
+  const int64_t unit = 4 * kTile;            // tokens of one turn of the four waves
+  const int64_t units = std::max<int64_t>(1, (a->max_len + unit - 1) / unit);
+  const int64_t want = (int64_t)device_cus() * 8;
+  int64_t splits = std::min<int64_t>({(want + base - 1) / base, (units + 3) / 4, kMaxSplits});
+  splits = std::max<int64_t>(splits, 1);
+  const int64_t per = (units + splits - 1) / splits;
+  splits = (units + per - 1) / per;
+  a->splits = (int32_t)splits;
+  a->split_len = (int32_t)(per * unit);
+  if (splits == 1) return 0;
+  return (int64_t)a->batch * a->nq_tok * a->nq * splits * (a->hd + 2) * (int64_t)sizeof(float);
+}
+
+namespace {
+template <int HD>
+hipError_t launch_hd(const PagedAttnArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)(a.nq / a.nkv) * a.nq_tok;
+  const int64_t grid = (int64_t)a.batch * a.nkv * ((rows + kRows - 1) / kRows) * a.splits;
+  if (grid > 0x7FFFFFFFLL) return hipErrorNotSupported;
+  hipLaunchKernelGGL((attn_split<HD>), dim3((unsigned)grid), dim3(kBlock), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
+  hipLaunchKernelGGL((attn_join<HD>), dim3((unsigned)((n_rows + 3) / 4)), dim3(kBlock), 0, s, a);
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_paged_attn(const PagedAttnArgs& a, hipStream_t s) {
+  switch (a.hd) {
+    case 64: return launch_hd<64>(a, s);
+    case 128: return launch_hd<128>(a, s);
+    case 256: return launch_hd<256>(a, s);
+  }
+  return hipErrorNotSupported;
+}
+
+}  // namespace sc
