@@ -303,8 +303,9 @@ sc_status sc_cca_qk_conv(const sc_cca_desc* desc, const void* q, const void* k,
  * are bf16 (the page's core rejects other inputs); the state, the gates and
  * every sum are fp32.
  *   q, k    (T, num_k_heads * DK), v, out (T, num_v_heads * DV): rows of their
- *           strides, e.g. the column blocks of the conv's output rows; q and k
- *           16-byte aligned with strides a multiple of 8
+ *           strides, e.g. the column blocks of the conv's output rows; q, k and
+ *           v 16-byte aligned with strides a multiple of 8, out 8-byte
+ *           aligned with a stride a multiple of 4
  *   a, b    (T, num_v_heads), gate_dtype; A_log, dt_bias (num_v_heads) fp32
  *   state   (num_slots, num_v_heads, DV, DK) fp32, contiguous, 16-byte aligned
  * DK is 64 or 128, DV a multiple of 16 (SC_ERR_UNSUPPORTED otherwise; also

@@ -123,10 +123,13 @@ sc_status check_gdn_desc(const sc_gdn_desc* d) {
       d->b_row_stride < d->num_v_heads || d->state_indices_stride < 1)
     return SC_ERR_INVALID_ARG;
   if ((d->head_k_dim != 64 && d->head_k_dim != 128) || d->head_v_dim % 16 != 0 ||
-      d->q_row_stride % 8 != 0 || d->k_row_stride % 8 != 0)
+      d->q_row_stride % 8 != 0 || d->k_row_stride % 8 != 0 || d->v_row_stride % 8 != 0 ||
+      d->out_row_stride % 4 != 0)
     return SC_ERR_UNSUPPORTED;
-  // a head's state and a row of heads are addressed with 32-bit offsets
-  if (vw > (1 << 24) || kw > (1 << 24)) return SC_ERR_UNSUPPORTED;
+  // 64 rows are addressed with 32-bit byte offsets
+  if (d->q_row_stride >= (1 << 24) || d->k_row_stride >= (1 << 24) ||
+      d->v_row_stride >= (1 << 24) || d->out_row_stride >= (1 << 24))
+    return SC_ERR_UNSUPPORTED;
   return SC_OK;
 }
 
@@ -142,7 +145,7 @@ sc_status gdn_args(const sc_gdn_desc* d, const void* q, const void* k, const voi
   if (!q || !k || !v || !a || !b || !A_log || !dt_bias || !out || !slots || (!pool && num_slots > 0))
     return SC_ERR_NULL_ARG;
   if (out == q || out == k || out == v) return SC_ERR_INVALID_ARG;
-  if (!al16(q) || !al16(k) || !al16(pool)) return SC_ERR_UNSUPPORTED;
+  if (!al16(q) || !al16(k) || !al16(v) || !al8(out) || !al16(pool)) return SC_ERR_UNSUPPORTED;
   *g = sc::GdnArgs{};
   g->q = q;
   g->k = k;

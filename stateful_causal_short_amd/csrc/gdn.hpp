@@ -41,7 +41,8 @@ struct GdnWorkspace {
   static constexpr int64_t kFrags = 6;               // (row tile, k step) pairs at or below the diagonal
   static constexpr int64_t kT = kFrags * 3 * kFrag;
   static constexpr int64_t kP = kFrags * 2 * kFrag;
-  static constexpr int64_t kVec = 5 * kGdnChunk * 4; // c1..c4 and the chunk's decay
+  static constexpr int64_t kDecay = 3 * kGdnChunk * 4;
+  static constexpr int64_t kVec = 4 * kGdnChunk * 4; // three row factors, the chunk's decay
   static constexpr int64_t kHead = kT + kP + kVec;
   static int64_t bytes(int64_t n_chunks, int64_t hk, int64_t hv, int64_t dk) {
     return n_chunks * (hv * kHead + hk * dk * kGdnChunk * 2);

@@ -125,6 +125,9 @@ PREFILLS = [  # hk, hv, dk, dv, lengths, gates, strong, pad
     (4, 8, 128, 128, [3] * 70, "bf16", False, 0),
     (1, 1, 128, 32, [1000], "bf16", False, 0),
     (16, 32, 128, 128, [129, 40], "bf16", False, 0),
+    (8, 16, 64, 80, [65, 2, 0, 190] + [7] * 20, "f32", True, 8),
+    (2, 4, 128, 16, [1, 70, 64] * 24, "bf16", False, 0),
+    (4, 12, 64, 128, [100, 33, 1], "bf16", True, 16),
 ]
 
 
