@@ -105,53 +105,99 @@ __device__ __forceinline__ Chunk chunk_of(const GdnArgs& a, int id) {
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// gdn_chunk: T and P of one (chunk, value head), four waves.
+// gdn_chunk: T and P of one (chunk, value head), four waves; bound by the
+// latency of its steps, so that they are few and short.
 //
-// Wave w owns rows 16w..16w+15. K K^T and Q K^T are 16x16x32 bf16 products of
-// raw rows read from global memory as MFMA operands (both operands of K K^T
-// have the same lane layout). The unit lower triangular inverse goes by
-// blocks: the four 16 x 16 diagonal blocks by forward substitution, a lane per
-// column, then T_ij = -T_ii (A_ij T_jj) at 16 and at 32 on fp32 MFMA.
+// Wave w owns rows 16w..16w+15. The products are taken transposed, K_j K_w^T
+// and K_j Q_w^T (16x16x32 bf16): a lane then holds one row t and four adjacent
+// columns s, which is how the scan's operands are laid out, so P goes to the
+// workspace from registers, and A to LDS in 16-byte rows. The unit lower
+// triangular inverse goes by blocks: the four 16 x 16 diagonal blocks by forward
+// substitution, a lane per column of each, with the row's elements broadcast
+// over 16 lanes; then T_ij = -T_ii (A_ij T_jj) at 16 and at 32 on fp32 MFMA, the
+// inner product staying in registers (an accumulator tile is a right operand of
+// 16x16x4 products whose step i sums over rows 4 g + i).
 // The first value head of a key head also writes the keys transposed, as the
 // scan's state update multiplies by them.
 // ---------------------------------------------------------------------------
+
+// Lane n of each 16, in all of them.
+template <int N>
+__device__ __forceinline__ float row16_bcast(float x) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + N, 0xF, 0xF, true));
+}
+// x_i = (i == column) + sum_{j<i} row_i[j] x_j, for rows held across 16 lanes.
+template <int I, int J>
+__device__ __forceinline__ float substitute(const float (&row)[16], const float (&x)[16], float s) {
+  if constexpr (J < I) return substitute<I, J + 1>(row, x, fmaf(row16_bcast<J>(row[I]), x[J], s));
+  else return s;
+}
+template <int I>
+__device__ __forceinline__ void substitute_rows(const float (&row)[16], float (&x)[16], int col) {
+  if constexpr (I < 16) {
+    x[I] = substitute<I, 0>(row, x, I == col ? 1.f : 0.f);
+    substitute_rows<I + 1>(row, x, col);
+  }
+}
+
+// x plus what another lane holds (DPP control), in the rows of the mask.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_lane(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+  return x + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// Sum of this lane's value and all before it.
+__device__ __forceinline__ double wave_running_sum(double x) {
+  x = add_lane<0x111, 0xF>(x);      // 1, 2, 4 and 8 lanes before, within 16
+  x = add_lane<0x112, 0xF>(x);
+  x = add_lane<0x114, 0xF>(x);
+  x = add_lane<0x118, 0xF>(x);
+  x = add_lane<0x142, 0xA>(x);      // lane 15 of the 16 before
+  return add_lane<0x143, 0xC>(x);   // lane 31
+}
+
 template <int DK>
-__global__ __launch_bounds__(kBlock) void gdn_chunk(GdnArgs a) {
+__global__ __launch_bounds__(kBlock, 4) void gdn_chunk(GdnArgs a) {
   constexpr int KS = DK / 32;
   constexpr int LD = 68;                      // fp32 row stride of the LDS matrices
+  constexpr int LK = DK + 8;                  // row stride of the keys
+  // the keys are read before T is written
+  constexpr int kKeyBytes = CH * LK * 2, kMatBytes = CH * LD * 4;
+  __shared__ __align__(16) char kt_mem[kKeyBytes > kMatBytes ? kKeyBytes : kMatBytes];
   __shared__ __align__(16) float Am[CH * LD];
-  __shared__ __align__(16) float Tm[CH * LD];
-  __shared__ double Gs[CH];
-  __shared__ __align__(16) float beta_s[CH];
-  __shared__ float rk_s[CH], rq_s[CH];
-  __shared__ __align__(16) uint16_t Kl[CH * (DK + 8)];
+  __shared__ __align__(16) double Gs[CH];
+  __shared__ __align__(16) float beta_s[CH], rk_s[CH], rq_s[CH];
+  uint16_t* const Kl = (uint16_t*)kt_mem;
+  float* const Tm = (float*)kt_mem;
 
   const int h = (int)(blockIdx.x % (unsigned)a.hv);
   const int id = (int)(blockIdx.x / (unsigned)a.hv);
   const Chunk c = chunk_of(a, id);
   if (c.n == 0) return;
   const int rep = a.hv / a.hk, hk = h / rep;
-  const int lane = (int)(threadIdx.x & 63), w = (int)(threadIdx.x >> 6);
+  const int lane = (int)(threadIdx.x & 63);
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l16 = lane & 15, lg = lane >> 4;
   const bool put_kt = h == hk * rep;
 
   // rows as MFMA operands: lane holds row l16 of a tile, 8 values from 8 lg
-  auto row_frag = [&](const void* p, int64_t rs, int t, int ks) {
-    u32x4 v = {0, 0, 0, 0};
-    if (t < c.n)
-      v = ld16((const uint16_t*)p + (int64_t)(c.row0 + t) * rs + hk * DK + ks * 32 + lg * 8);
-    return v;
-  };
   u32x4 kw[KS], qw[KS];
+  const int my_row = w * 16 + l16;
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
-    kw[ks] = row_frag(a.k, a.k_rs, w * 16 + l16, ks);
-    qw[ks] = row_frag(a.q, a.q_rs, w * 16 + l16, ks);
+    kw[ks] = qw[ks] = u32x4{0, 0, 0, 0};
+    if (my_row < c.n) {
+      const int64_t row = c.row0 + my_row;
+      kw[ks] = ld16((const uint16_t*)a.k + row * a.k_rs + hk * DK + ks * 32 + lg * 8);
+      qw[ks] = ld16((const uint16_t*)a.q + row * a.q_rs + hk * DK + ks * 32 + lg * 8);
+    }
   }
-
-  // gates: wave 0, a lane per token; the running sum in fp64, so that the
-  // difference of two of a chunk's sums keeps fp32 accuracy whatever came
-  // before. A decay below e^-110 is zero in fp32 already.
+  // gates: wave 0, a lane per token; the running sum in fp64 (of base 2
+  // exponents), so that the difference of two of a chunk's sums keeps fp32
+  // accuracy whatever came before. A decay below e^-110 is zero in fp32 already.
   if (w == 0) {
     float g = 0.f, be = 0.f;
     if (lane < c.n) {
@@ -159,20 +205,15 @@ __global__ __launch_bounds__(kBlock) void gdn_chunk(GdnArgs a) {
       g = g < -110.f ? -110.f : g;
       be = gdn_beta(a, c.row0 + lane, h);
     }
-    double s = g;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double o = __shfl_up(s, d);
-      if (lane >= d) s += o;
-    }
-    Gs[lane] = s;
+    Gs[lane] = wave_running_sum((double)g * 1.4426950408889634);
     beta_s[lane] = be;
   }
-  // unit lengths
+  // unit lengths; keys to LDS
   {
     float kk = 0.f, qq = 0.f;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+    for (int ks = 0; ks < KS; ++ks) {
+      *(u32x4*)(Kl + my_row * LK + ks * 32 + lg * 8) = kw[ks];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         kk = fmaf(lo_f(kw[ks][e]), lo_f(kw[ks][e]), kk);
@@ -180,90 +221,56 @@ __global__ __launch_bounds__(kBlock) void gdn_chunk(GdnArgs a) {
         qq = fmaf(lo_f(qw[ks][e]), lo_f(qw[ks][e]), qq);
         qq = fmaf(hi_f(qw[ks][e]), hi_f(qw[ks][e]), qq);
       }
+    }
     kk += __shfl_xor(kk, 16);
     kk += __shfl_xor(kk, 32);
     qq += __shfl_xor(qq, 16);
     qq += __shfl_xor(qq, 32);
     if (lg == 0) {
-      rk_s[w * 16 + l16] = a.l2norm ? rsqrtf(kk + kL2Eps) : 1.f;
-      rq_s[w * 16 + l16] = a.scale * (a.l2norm ? rsqrtf(qq + kL2Eps) : 1.f);
-    }
-  }
-  if (put_kt) {
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-      *(u32x4*)(Kl + (w * 16 + l16) * (DK + 8) + ks * 32 + lg * 8) = kw[ks];
-  }
-  // raw products: tiles (w, j), j <= w
-  f32x4 kk[4], qk[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    kk[j] = qk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (j <= w) {
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const u32x4 bj = row_frag(a.k, a.k_rs, j * 16 + l16, ks);
-        kk[j] = mfma_bf16(kw[ks], bj, kk[j]);
-        qk[j] = mfma_bf16(qw[ks], bj, qk[j]);
-      }
+      rk_s[my_row] = a.l2norm ? rsqrtf(kk + kL2Eps) : 1.f;
+      rq_s[my_row] = a.scale * (a.l2norm ? rsqrtf(qq + kL2Eps) : 1.f);
     }
   }
   __syncthreads();
 
   char* const ws = a.ws + ((int64_t)id * a.hv + h) * GdnWorkspace::kHead;
+  // raw products and their factors, column tiles j <= w
+  f32x4 P[4];
+  {
+    const double gt = Gs[my_row];
+    const float rq = rq_s[my_row], bk = beta_s[my_row] * rk_s[my_row];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      P[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (j > w) continue;
+      f32x4 kk = P[j], qk = P[j];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const u32x4 kj = *(const u32x4*)(Kl + (j * 16 + l16) * LK + ks * 32 + lg * 8);
+        kk = mfma_bf16(kj, kw[ks], kk);
+        qk = mfma_bf16(kj, qw[ks], qk);
+      }
+      const f32x4 rk = *(const f32x4*)(rk_s + j * 16 + lg * 4);
+      f32x4 A;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int s = j * 16 + lg * 4 + i;
+        const float d = __builtin_amdgcn_exp2f((float)(gt - Gs[s])) * rk[i];
+        A[i] = s < my_row ? bk * d * kk[i] : 0.f;
+        P[j][i] = s <= my_row ? rq * d * qk[i] : 0.f;
+      }
+      *(f32x4*)(Am + my_row * LD + j * 16 + lg * 4) = A;
+    }
+  }
   // row factors of the scan
   if (w == 0) {
     float* vec = (float*)(ws + GdnWorkspace::kT + GdnWorkspace::kP);
-    const float eg = expf((float)Gs[lane]), rk = rk_s[lane];
-    vec[lane] = eg * rk;                                              // of S k
-    vec[CH + lane] = rk * expf((float)(Gs[CH - 1] - Gs[lane]));       // of U in the update
-    vec[2 * CH + lane] = rq_s[lane] * eg;                             // of S q
-    if (lane == 0) vec[3 * CH] = expf((float)Gs[CH - 1]);             // of S
+    const float eg = __builtin_amdgcn_exp2f((float)Gs[lane]), rk = rk_s[lane];
+    vec[lane] = eg * rk;                                                             // of S k
+    vec[CH + lane] = rk * __builtin_amdgcn_exp2f((float)(Gs[CH - 1] - Gs[lane]));    // of U in the update
+    vec[2 * CH + lane] = rq_s[lane] * eg;                                            // of S q
+    if (lane == 0) vec[3 * CH] = __builtin_amdgcn_exp2f((float)Gs[CH - 1]);          // of S
   }
-  // A into LDS, P into LDS (Tm, until T overwrites it)
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = w * 16 + lg * 4 + i, s = j * 16 + l16;
-      float av = 0.f, pv = 0.f;
-      if (s <= t) {
-        const float d = expf((float)(Gs[t] - Gs[s])) * rk_s[s];
-        if (s < t) av = beta_s[t] * rk_s[t] * d * kk[j][i];
-        pv = rq_s[t] * d * qk[j][i];
-      }
-      Am[t * LD + s] = av;
-      Tm[t * LD + s] = pv;
-    }
-  }
-  __syncthreads();
-  // matrix rows as operand fragments, in the scan's order of tokens: N parts of
-  // 4 adjacent values from column 32 ks + 4 lg and 4 from 16 further on, each
-  // column times `col` if given
-  auto put_frags = [&](auto parts, const float* m, char* dst, const float* col) {
-    constexpr int N = decltype(parts)::value;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      if (w < 2 && ks == 1) continue;
-      const float* p = m + (w * 16 + l16) * LD + ks * 32 + lg * 4;
-      f32x4 x = *(const f32x4*)p, y = *(const f32x4*)(p + 16);
-      if (col) {
-        const f32x4 cx = *(const f32x4*)(col + ks * 32 + lg * 4),
-                    cy = *(const f32x4*)(col + ks * 32 + lg * 4 + 16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] *= cx[e];
-          y[e] *= cy[e];
-        }
-      }
-      u32x4 part[N];
-      split8<N>(x, y, part);
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        *(u32x4*)(dst + (frag_of(w, ks) * N + n) * GdnWorkspace::kFrag + lane * 16) = part[n];
-    }
-  };
-  put_frags(std::integral_constant<int, 2>{}, Tm, ws + GdnWorkspace::kT, nullptr);
   if (put_kt) {
     // keys transposed, in the scan's orders of key dims (row l16 of state tile
     // m) and of tokens
@@ -274,74 +281,104 @@ __global__ __launch_bounds__(kBlock) void gdn_chunk(GdnArgs a) {
       const int f = w * (DK / 32) + i;        // fragment (tile m, k step ks)
       const int m = f >> 1, ks = f & 1;
       const int dim = (m >> 1) * 32 + (l16 >> 2) * 8 + (m & 1) * 4 + (l16 & 3);
-      const uint16_t* p = Kl + (ks * 32 + lg * 4) * (DK + 8) + dim;
+      const uint16_t* p = Kl + (ks * 32 + lg * 4) * LK + dim;
       u32x4 v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-      {
-        const uint16_t* t = p + ((e >> 1) * 16 + (e & 1) * 2) * (DK + 8);
-        v[e] = (uint32_t)t[0] | ((uint32_t)t[DK + 8] << 16);
+      for (int e = 0; e < 4; ++e) {
+        const uint16_t* t = p + ((e >> 1) * 16 + (e & 1) * 2) * LK;
+        v[e] = (uint32_t)t[0] | ((uint32_t)t[LK] << 16);
       }
       *(u32x4*)(kt + f * GdnWorkspace::kFrag + lane * 16) = v;
     }
   }
-  __syncthreads();
-  // T: zero above the diagonal blocks; diagonal blocks by substitution
-  for (int i = (int)threadIdx.x; i < CH * LD / 4; i += kBlock)
-    *(f32x4*)(Tm + i * 4) = f32x4{0.f, 0.f, 0.f, 0.f};
-  __syncthreads();
+  __syncthreads();                            // A is there, and the keys are done with
+  // diagonal blocks of T by substitution (wave 0; lane: column l16 of block
+  // lg); the others write P meanwhile
   if (w == 0) {
-    const float* ab = Am + lg * 16 * LD + lg * 16;
-    float x[16];
+    float row[16], x[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float s = i == l16 ? 1.f : 0.f;
-#pragma unroll
-      for (int j = 0; j < i; ++j) s = fmaf(-ab[i * LD + j], x[j], s);
-      x[i] = s;
-    }
+    for (int i = 0; i < 16; ++i) row[i] = -Am[(lg * 16 + i) * LD + lg * 16 + l16];
+    substitute_rows<0>(row, x, l16);
 #pragma unroll
     for (int i = 0; i < 16; ++i) Tm[(lg * 16 + i) * LD + lg * 16 + l16] = x[i];
   }
-  __syncthreads();
-  // 16 x 16 product of LDS blocks at (rx, cx) of X and (ry, cy) of Y
-  auto mul16 = [&](const float* X, int rx, int cx, const float* Y, int ry, int cy, f32x4 acc) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      acc = mfma_f32(X[(rx * 16 + l16) * LD + cx * 16 + k * 4 + lg],
-                     Y[(ry * 16 + k * 4 + lg) * LD + cy * 16 + l16], acc);
+  for (int ks = 0; ks < 2; ++ks) {
+    if (ks == 1 && w < 2) continue;
+    u32x4 part[2];
+    split8<2>(P[2 * ks], P[2 * ks + 1], part);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      *(u32x4*)(ws + GdnWorkspace::kT + (frag_of(w, ks) * 2 + n) * GdnWorkspace::kFrag + lane * 16) =
+          part[n];
+  }
+  // blocks (0, 1) and (2, 3) of T, which the operands of 32 columns take in
+  if (w == 1 || w == 2) {
+    const int r0 = (w - 1) * 32 + l16, c0 = (w - 1) * 32 + 16 + lg * 4;
+    *(f32x4*)(Tm + r0 * LD + c0) = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  __syncthreads();
+  // X(rx, cx) Y + acc for a block X in LDS and an accumulator tile Y
+  auto mul_reg = [&](const float* X, int rx, int cx, f32x4 y, f32x4 acc) {
+    const f32x4 x = *(const f32x4*)(X + (rx * 16 + l16) * LD + cx * 16 + lg * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc = mfma_f32(x[i], y[i], acc);
     return acc;
   };
-  auto put16 = [&](float* X, int r, int col, f32x4 v, float sign) {
+  auto get16 = [&](const float* X, int r, int col) {
+    f32x4 y;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) X[(r * 16 + lg * 4 + i) * LD + col * 16 + l16] = sign * v[i];
+    for (int i = 0; i < 4; ++i) y[i] = X[(r * 16 + lg * 4 + i) * LD + col * 16 + l16];
+    return y;
+  };
+  auto put_neg16 = [&](float* X, int r, int col, f32x4 v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) X[(r * 16 + lg * 4 + i) * LD + col * 16 + l16] = -v[i];
   };
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  // blocks (1,0) and (3,2): the inner product goes where A's block was
+  // blocks (1,0) and (3,2)
   if (w < 2) {
     const int b = 2 * w;
-    put16(Am, b + 1, b, mul16(Am, b + 1, b, Tm, b, b, zero), 1.f);
+    const f32x4 y = mul_reg(Am, b + 1, b, get16(Tm, b, b), zero);
+    put_neg16(Tm, b + 1, b, mul_reg(Tm, b + 1, b + 1, y, zero));
   }
   __syncthreads();
-  if (w < 2) {
-    const int b = 2 * w;
-    put16(Tm, b + 1, b, mul16(Tm, b + 1, b + 1, Am, b + 1, b, zero), -1.f);
-  }
-  __syncthreads();
-  // the 32 x 32 block below: a wave per 16 x 16 tile
+  // the 32 x 32 block below: a wave per 16 x 16 tile (i, j)
   {
     const int i = 2 + (w >> 1), j = w & 1;
-    f32x4 y = mul16(Am, i, 1, Tm, 1, j, zero);     // Tm(0, 1) is zero
-    if (j == 0) y = mul16(Am, i, 0, Tm, 0, 0, y);
-    __syncthreads();
-    put16(Am, i, j, y, 1.f);
-    __syncthreads();
-    f32x4 z = mul16(Tm, i, 2, Am, 2, j, zero);
-    if (i == 3) z = mul16(Tm, 3, 3, Am, 3, j, z);
-    put16(Tm, i, j, z, -1.f);
+    const f32x4 t1 = get16(Tm, 1, j);
+    f32x4 t0 = zero;                           // block (0, 1) is zero
+    if (j == 0) t0 = get16(Tm, 0, 0);
+    f32x4 y2 = mul_reg(Am, 2, 1, t1, zero);
+    if (j == 0) y2 = mul_reg(Am, 2, 0, t0, y2);
+    f32x4 z = mul_reg(Tm, i, 2, y2, zero);
+    if (i == 3) {
+      f32x4 y3 = mul_reg(Am, 3, 1, t1, zero);
+      if (j == 0) y3 = mul_reg(Am, 3, 0, t0, y3);
+      z = mul_reg(Tm, 3, 3, y3, z);
+    }
+    put_neg16(Tm, i, j, z);
   }
   __syncthreads();
-  put_frags(std::integral_constant<int, 3>{}, Tm, ws, beta_s);
+  // T diag(beta) as operand fragments, in the scan's order of tokens: three
+  // parts of 4 adjacent values from column 32 ks + 4 lg and 4 from 16 further on
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    if (ks == 1 && w < 2) continue;
+    const int c0 = ks * 32 + lg * 4;
+    f32x4 x = *(const f32x4*)(Tm + my_row * LD + c0), y = *(const f32x4*)(Tm + my_row * LD + c0 + 16);
+    const f32x4 bx = *(const f32x4*)(beta_s + c0), by = *(const f32x4*)(beta_s + c0 + 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] *= bx[e];
+      y[e] *= by[e];
+    }
+    u32x4 part[3];
+    split8<3>(x, y, part);
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+      *(u32x4*)(ws + (frag_of(w, ks) * 3 + n) * GdnWorkspace::kFrag + lane * 16) = part[n];
+  }
 }
 
 // ---------------------------------------------------------------------------
