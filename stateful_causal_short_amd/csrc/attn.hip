@@ -37,22 +37,25 @@ constexpr float kNone = -3.0e38f;   // running maximum before any token
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Whether one of four bf16 values is infinite or NaN.
-__device__ __forceinline__ bool any_special(uint2 w) {
-  auto special = [](uint32_t x) {
-    return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
-  };
-  return special(w.x) || special(w.y);
+// Two bf16 values, infinities and NaN replaced by zero.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
+  const uint32_t lo = (x & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu;
+  return ((x & 0x7F800000u) == 0x7F800000u ? 0u : x & 0xFFFF0000u) | lo;
 }
+
+// N adjacent bf16 values (4 or 8), one load.
+template <int N>
+using ValueRun = uint32_t __attribute__((ext_vector_type(N / 2)));
 
 }  // namespace
 
 // Workspace: for each (query row, split) the maximum, the sum and hd values.
 template <int HD>
-__global__ __launch_bounds__(kBlock) void attn_split(PagedAttnArgs a) {
+__global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAttnArgs a) {
   constexpr int KS = HD / 32;               // score products per tile
   constexpr int VPL = HD / 16;              // values of a token's row per lane
-  constexpr int VW = VPL / 4;               // ... in 8-byte words
+  constexpr int VR = VPL < 8 ? VPL : 8;     // ... in runs of one load, 16 VR apart
+  constexpr int VW = VPL / VR;
   __shared__ __align__(16) float Ol[3][kRows * HD];
   __shared__ float ml[3][kRows], ll[3][kRows];
 
@@ -69,8 +72,16 @@ __global__ __launch_bounds__(kBlock) void attn_split(PagedAttnArgs a) {
   const int lane = (int)(threadIdx.x & 63);
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l16 = lane & 15, lg = lane >> 4;
+  const int t_lo = split * a.split_len;
+  // Page ids run two tiles ahead of their use: a load that waits for another
+  // load waits for the memory queue twice. They do not wait for the length
+  // either: a tile below max_len has an entry in the table.
+  const int32_t* const table = a.table + (int64_t)r * a.table_rs;
+  auto page_of = [&](int t) { return t < a.max_len ? table[t / a.block_size] : -1; };
+  int t0 = t_lo + w * kTile;
+  int page = page_of(t0), page_next = page_of(t0 + 4 * kTile);
   const int len = min(max(a.lens[r], 0), a.max_len);
-  const int t_lo = split * a.split_len, t_hi = min(len, t_lo + a.split_len);
+  const int t_hi = min(len, t_lo + a.split_len);
   if (split > 0 && t_lo >= len) return;      // the join does not read such a split
 
   // this lane's query row: head kvh * group + g of new token j
@@ -88,47 +99,57 @@ __global__ __launch_bounds__(kBlock) void attn_split(PagedAttnArgs a) {
       qf[s] = ld16((const uint16_t*)a.q + q_row * a.q_rs + (int64_t)head * HD + s * 32 + lg * 8);
   }
 
+  const int first_new = len - a.nq_tok + 1;    // from here on only later drafts see
+  bool odd = false;                            // a non-finite value was among those
   float m = kNone, l = 0.f;
   f32x4 O[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) O[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const float c = a.scale * 1.4426950408889634f;
-  const int32_t* const table = a.table + (int64_t)r * a.table_rs;
   const uint16_t* const kbase = (const uint16_t*)a.kc.p + (int64_t)kvh * a.kc.head_s;
   const uint16_t* const vbase = (const uint16_t*)a.vc.p + (int64_t)kvh * a.vc.head_s;
 
-  struct Tile {
-    u32x4 k[KS];
-    uint2 v[4][VW];
-    bool ok;
-  };
   // A tile lies in one page (pages are multiples of 16 tokens). A page id
   // outside the cache makes the tile invisible.
-  auto load = [&](Tile& x, int t0) {
-    const int b = t0 / a.block_size;
-    const int page = table[b];
-    x.ok = page >= 0 && page < a.num_blocks;
-    const int64_t pg = x.ok ? page : 0;
-    const int in = t0 - b * a.block_size;
+  auto load_k = [&](u32x4* k, int64_t pg, int in) {
     const uint16_t* kp = kbase + pg * a.kc.block_s + (int64_t)(in + l16) * a.kc.token_s + lg * 8;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) x.k[s] = ld16(kp + s * 32);
-    const uint16_t* vp = vbase + pg * a.vc.block_s + (int64_t)(in + lg * 4) * a.vc.token_s + l16 * 4;
+    for (int s = 0; s < KS; ++s) k[s] = ld16(kp + s * 32);
+  };
+  auto load_v = [&](ValueRun<VR> (*v)[VW], int64_t pg, int in) {
+    const uint16_t* vp = vbase + pg * a.vc.block_s + (int64_t)(in + lg * 4) * a.vc.token_s + l16 * VR;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int u = 0; u < VW; ++u) x.v[i][u] = *(const uint2*)(vp + (int64_t)i * a.vc.token_s + u * 64);
+      for (int u = 0; u < VW; ++u)
+        v[i][u] = *(const ValueRun<VR>*)(vp + (int64_t)i * a.vc.token_s + u * 16 * VR);
   };
-  Tile cur, nxt;
-  int t0 = t_lo + w * kTile;
-  if (t0 < t_hi) load(cur, t0);
+  // The next tile's keys and values are loaded as soon as this one's have been
+  // used; four workgroups a CU (128 registers) hide what is left of the latency.
+  struct {
+    u32x4 k[KS];
+    ValueRun<VR> v[4][VW];
+    bool ok;
+  } cur;
+  auto in_cache = [&](int pg) { return pg >= 0 && pg < a.num_blocks; };
+  int64_t pg = in_cache(page) ? page : 0;
+  if (t0 < t_hi) {
+    cur.ok = in_cache(page);
+    load_k(cur.k, pg, t0 % a.block_size);
+    load_v(cur.v, pg, t0 % a.block_size);
+  }
   for (; t0 < t_hi; t0 += 4 * kTile) {
-    if (t0 + 4 * kTile < t_hi) load(nxt, t0 + 4 * kTile);
+    const bool more = t0 + 4 * kTile < t_hi;
+    const bool next_ok = in_cache(page_next);
+    const int in = (t0 + 4 * kTile) % a.block_size;
+    pg = next_ok ? page_next : 0;
+    page_next = page_of(t0 + 8 * kTile);
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
       s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cur.k[ks]),
                                                   __builtin_bit_cast(bf16x8, qf[ks]), s, 0, 0, 0);
+    if (more) load_k(cur.k, pg, in);
     float top = kNone;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -159,64 +180,69 @@ __global__ __launch_bounds__(kBlock) void attn_split(PagedAttnArgs a) {
       l += p[i];
     }
     // Value rows behind the visible ones hold anything, NaN included, which a
-    // weight of 0 would not undo: they count as zeros. So do the non-finite
-    // values of a row that only the later drafts see; those are added apart.
-    uint32_t odd = 0;
-    if (a.nq_tok > 1 && t0 + kTile > len - a.nq_tok + 1) {
+    // weight of 0 would not undo: they count as zeros. So do non-finite values
+    // that only later drafts see; they are added after the loop, to those alone.
+    if (a.nq_tok > 1 && t0 + kTile > first_new) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bool bad = false;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int u = 0; u < VW; ++u) bad = bad || any_special(cur.v[i][u]);
-        if (bad && t0 + lg * 4 + i > len - a.nq_tok) odd |= 1u << i;
-      }
-      if (__any(odd != 0)) {
-        for (int tt = 0; tt < kTile; ++tt) {
-          const int from = (tt >> 2) * 16, t = t0 + tt;
+        for (int u = 0; u < VW; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i != (tt & 3)) continue;
-            // a row of 16 lanes holds a token: odd if any of its lanes is
-            if (!(__ballot((odd >> i) & 1) >> from & 0xFFFF)) continue;
-#pragma unroll
-            for (int ii = 0; ii < 4; ++ii) {
-              const float pw = __shfl(p[i], from + lg * 4 + ii);
-              const bool sees = __shfl(limit, lg * 4 + ii) >= t && cur.ok && t < t_hi;
-#pragma unroll
-              for (int u = 0; u < VW; ++u) {
-                const uint32_t x0 = __shfl((int)cur.v[i][u].x, from + l16);
-                const uint32_t x1 = __shfl((int)cur.v[i][u].y, from + l16);
-                if (sees) {
-                  O[u * 4 + 0][ii] += pw * __uint_as_float(x0 << 16);
-                  O[u * 4 + 1][ii] += pw * __uint_as_float(x0 & 0xFFFF0000u);
-                  O[u * 4 + 2][ii] += pw * __uint_as_float(x1 << 16);
-                  O[u * 4 + 3][ii] += pw * __uint_as_float(x1 & 0xFFFF0000u);
-                }
-              }
+          for (int e = 0; e < VR / 2; ++e) {
+            const uint32_t x = cur.v[i][u][e], y = finite_pair(x);
+            if (y != x && t0 + lg * 4 + i >= first_new && t0 + lg * 4 + i < t_hi && cur.ok) {
+              cur.v[i][u][e] = y;
+              odd = true;
             }
-            if (lg == tt >> 2) odd |= 16u << i;      // the whole row was added
           }
-        }
-      }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool live = cur.ok && t0 + lg * 4 + i < t_hi && !((odd >> (4 + i)) & 1);
+      const bool live = cur.ok && t0 + lg * 4 + i < t_hi;
 #pragma unroll
       for (int u = 0; u < VW; ++u) {
-        const uint32_t x0 = live ? cur.v[i][u].x : 0u, x1 = live ? cur.v[i][u].y : 0u;
-        O[u * 4 + 0] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], __uint_as_float(x0 << 16), O[u * 4 + 0], 0, 0, 0);
-        O[u * 4 + 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], __uint_as_float(x0 & 0xFFFF0000u), O[u * 4 + 1], 0, 0, 0);
-        O[u * 4 + 2] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], __uint_as_float(x1 << 16), O[u * 4 + 2], 0, 0, 0);
-        O[u * 4 + 3] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], __uint_as_float(x1 & 0xFFFF0000u), O[u * 4 + 3], 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < VR / 2; ++e) {
+          const uint32_t x = live ? cur.v[i][u][e] : 0u;
+          O[u * VR + 2 * e] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+              p[i], __uint_as_float(x << 16), O[u * VR + 2 * e], 0, 0, 0);
+          O[u * VR + 2 * e + 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+              p[i], __uint_as_float(x & 0xFFFF0000u), O[u * VR + 2 * e + 1], 0, 0, 0);
+        }
       }
     }
-    cur = nxt;
+    if (more) load_v(cur.v, pg, in);
+    cur.ok = next_ok;
+  }
+  if (__any(odd)) {
+#pragma unroll 1
+    for (int t = max(first_new, t_lo); t < t_hi; ++t) {
+      if ((((t - t_lo) / kTile) & 3) != w) continue;
+      const int b = t / a.block_size, page = table[b];
+      if (page < 0 || page >= a.num_blocks) continue;
+      const uint16_t* vp = vbase + page * a.vc.block_s + (int64_t)(t - b * a.block_size) * a.vc.token_s + l16 * VR;
+      bool sees[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sees[i] = __shfl(limit, lg * 4 + i) >= t;
+#pragma unroll
+      for (int u = 0; u < VW; ++u) {
+        const ValueRun<VR> run = *(const ValueRun<VR>*)(vp + u * 16 * VR);
+#pragma unroll
+        for (int e = 0; e < VR; ++e) {
+          const uint32_t x = run[e / 2];
+          const float y = __uint_as_float(e & 1 ? x & 0xFFFF0000u : x << 16);
+          const bool add = !(fabsf(y) < INFINITY);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) O[u * VR + e][i] += add && sees[i] ? y : 0.f;
+        }
+      }
+    }
   }
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
-  // join the four waves: wave 0 takes in the others' parts. O[d] of a lane is
-  // value u*64 + l16*4 + e (d = 4u + e) of rows 4 lg + i.
+  // join the four waves: wave 0 takes in the others' parts. O[u VR + e] of a
+  // lane is value (16 u + l16) VR + e of rows 4 lg + i; F: in fours.
+  constexpr int F = VR / 4;
   if (w > 0) {
     if (lg == 0) {
       ml[w - 1][l16] = m;
@@ -225,8 +251,8 @@ __global__ __launch_bounds__(kBlock) void attn_split(PagedAttnArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int u = 0; u < VW; ++u)
-        *(f32x4*)&Ol[w - 1][(lg * 4 + i) * HD + u * 64 + l16 * 4] =
+      for (int u = 0; u < VW * F; ++u)
+        *(f32x4*)&Ol[w - 1][(lg * 4 + i) * HD + (u / F * 16 + l16) * VR + u % F * 4] =
             f32x4{O[u * 4][i], O[u * 4 + 1][i], O[u * 4 + 2][i], O[u * 4 + 3][i]};
   }
   __syncthreads();
@@ -258,8 +284,8 @@ __global__ __launch_bounds__(kBlock) void attn_split(PagedAttnArgs a) {
     const int jj = rr / group, hh = kvh * group + rr - jj * group;
     const int64_t qr = (int64_t)r * a.nq_tok + jj;
 #pragma unroll
-    for (int u = 0; u < VW; ++u) {
-      const int at = src * HD + u * 64 + l16 * 4;
+    for (int u = 0; u < VW * F; ++u) {
+      const int col = (u / F * 16 + l16) * VR + u % F * 4, at = src * HD + col;
       const f32x4 a1 = *(const f32x4*)&Ol[0][at], a2 = *(const f32x4*)&Ol[1][at],
                   a3 = *(const f32x4*)&Ol[2][at];
       f32x4 y;
@@ -268,10 +294,10 @@ __global__ __launch_bounds__(kBlock) void attn_split(PagedAttnArgs a) {
         y[e] = (O[u * 4 + e][i] * g0 + a1[e] * g1 + a2[e] * g2 + a3[e] * g3) * gi;
       if (rr < rows) {
         if (a.splits > 1) {
-          *(f32x4*)(wo + ((qr * a.nq + hh) * a.splits + split) * HD + u * 64 + l16 * 4) = y;
+          *(f32x4*)(wo + ((qr * a.nq + hh) * a.splits + split) * HD + col) = y;
         } else {
           f32x2 y0 = {y[0], y[1]}, y1 = {y[2], y[3]};
-          *(uint2*)((uint16_t*)a.out + qr * a.out_rs + (int64_t)hh * HD + u * 64 + l16 * 4) =
+          *(uint2*)((uint16_t*)a.out + qr * a.out_rs + (int64_t)hh * HD + col) =
               uint2{__builtin_bit_cast(uint32_t, __builtin_convertvector(y0, bf16x2)),
                     __builtin_bit_cast(uint32_t, __builtin_convertvector(y1, bf16x2))};
         }
@@ -280,14 +306,16 @@ __global__ __launch_bounds__(kBlock) void attn_split(PagedAttnArgs a) {
   }
 }
 
-// Adds the splits of a query row: a wave per row, hd/64 values a lane.
+// Adds the splits of a query row: a workgroup per row, its waves take splits in
+// turn (all loads of a wave in flight together), hd/64 values a lane.
 template <int HD>
 __global__ __launch_bounds__(kBlock) void attn_join(PagedAttnArgs a) {
   constexpr int N = HD / 64;
+  __shared__ float part_s[3][HD];
   const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= n_rows) return;
+  const int64_t row = blockIdx.x;
   const int lane = (int)(threadIdx.x & 63);
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int64_t q_row = row / a.nq;
   const int head = (int)(row - q_row * a.nq);
   const int r = (int)(q_row / a.nq_tok);
@@ -296,26 +324,35 @@ __global__ __launch_bounds__(kBlock) void attn_join(PagedAttnArgs a) {
   const float* ml = a.ws + row * a.splits * 2;
   const float* part = a.ws + n_rows * a.splits * 2 + row * a.splits * HD + lane * N;
   const float mine = lane < n ? ml[lane * 2] : kNone;
+  float lt = lane < n ? ml[lane * 2 + 1] : 0.f;
+  float y[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) y[e] = 0.f;
   float mt = mine;
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) mt = fmaxf(mt, __shfl_xor(mt, d));
   const float f = lane < n ? exp2_(mine - mt) : 0.f;
-  float lt = lane < n ? ml[lane * 2 + 1] * f : 0.f;
+  lt *= f;
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) lt += __shfl_xor(lt, d);
-  float y[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) y[e] = 0.f;
-  for (int s = 0; s < n; ++s) {
+#pragma unroll 4
+  for (int s = w; s < n; s += 4) {
     const float fs = __shfl(f, s);
 #pragma unroll
     for (int e = 0; e < N; ++e) y[e] = fmaf(part[(int64_t)s * HD + e], fs, y[e]);
   }
+  if (w > 0) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) part_s[w - 1][lane * N + e] = y[e];
+  }
+  __syncthreads();
+  if (w > 0) return;
   const float inv = lt > 0.f ? 1.f / lt : 0.f;
   uint16_t* o = (uint16_t*)a.out + q_row * a.out_rs + (int64_t)head * HD + lane * N;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    f32x2 p = {y[e] * inv, 0.f};
+    const float t = (y[e] + part_s[0][lane * N + e]) + (part_s[1][lane * N + e] + part_s[2][lane * N + e]);
+    f32x2 p = {t * inv, 0.f};
     o[e] = (uint16_t)__builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
   }
 }
@@ -325,8 +362,12 @@ int64_t plan_paged_attn(PagedAttnArgs* a) {
   const int64_t base = (int64_t)a->batch * a->nkv * ((rows + kRows - 1) / kRows);
   const int64_t unit = 4 * kTile;            // tokens of one turn of the four waves
   const int64_t units = std::max<int64_t>(1, (a->max_len + unit - 1) / unit);
-  const int64_t want = (int64_t)device_cus() * 8;
-  int64_t splits = std::min<int64_t>({(want + base - 1) / base, (units + 3) / 4, kMaxSplits});
+  // Eight workgroups a CU, or sixteen where they come from the split alone
+  // (lengths differ, and a short request's splits end at once: 64 x 4 drafts
+  // over up to 8,192 tokens took 159 us with eight, 140 with sixteen or more);
+  // a split has 512 tokens or more.
+  const int64_t cus = device_cus(), want = base >= 4 * cus ? 8 * cus : 16 * cus;
+  int64_t splits = std::min<int64_t>({(want + base - 1) / base, (units + 7) / 8, kMaxSplits});
   splits = std::max<int64_t>(splits, 1);
   const int64_t per = (units + splits - 1) / splits;
   splits = (units + per - 1) / per;
@@ -346,7 +387,7 @@ hipError_t launch_hd(const PagedAttnArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
-  hipLaunchKernelGGL((attn_join<HD>), dim3((unsigned)((n_rows + 3) / 4)), dim3(kBlock), 0, s, a);
+  hipLaunchKernelGGL((attn_join<HD>), dim3((unsigned)n_rows), dim3(kBlock), 0, s, a);
   return hipGetLastError();
 }
 }  // namespace
