@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Tuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -146,7 +147,7 @@ def lib():
         L.sc_cca_qk_conv.restype = I32
         L.sc_cca_qk_conv.argtypes = [ctypes.POINTER(sc_cca_desc), P, P, P, P, P, P, P,
                                      P, P, P, P, P, I32, I32, P, I32, P, P, P, I64, P]
-        G = ctypes.POINTER(sc_gdn_desc)
+        G = P     # a descriptor's address, or its bytes
         L.sc_gdn_workspace_bytes.restype = I32
         L.sc_gdn_workspace_bytes.argtypes = [G, I32, I64, ctypes.POINTER(I64)]
         L.sc_gdn_prefill_varlen.restype = I32
@@ -156,10 +157,9 @@ def lib():
         L.sc_gdn_update.argtypes = [G, P, P, P, P, P, P, P, P, P, I32, P, P, I32, I32, P]
         L.sc_gdn_update_spec.restype = I32
         L.sc_gdn_update_spec.argtypes = [G, P, P, P, P, P, P, P, P, P, I32, P, P, I32, I32, P]
-        PC = ctypes.POINTER(sc_paged_cache)
-        PA = ctypes.POINTER(sc_paged_attn_desc)
+        PC = PA = P
         L.sc_qk_norm_rope.restype = I32
-        L.sc_qk_norm_rope.argtypes = [ctypes.POINTER(sc_qk_norm_desc), P, P, P, P, P, P, P, P, P,
+        L.sc_qk_norm_rope.argtypes = [P, P, P, P, P, P, P, P, P, P,
                                       P, PC, PC, I64, P]
         L.sc_paged_attn_workspace_bytes.restype = I32
         L.sc_paged_attn_workspace_bytes.argtypes = [PA, I32, I32, I32, ctypes.POINTER(I64)]
@@ -569,43 +569,82 @@ __all__ = ["lib", "ScError", "LIB_PATH", "EXPORTS", "sc_conv_desc", "sc_ckpt_des
            "sc_state_gather", "sc_state_scatter", "sc_cca_qk_conv"]
 
 
+# The calls below marshal a dozen small things each, and a decode step is as
+# long as its marshalling: descriptors are packed as bytes (the layout of the
+# structures above), and each tensor's shape and strides are read once.
+_GDN_DESC = struct.Struct("@7if7q")
+_QK_NORM_DESC = struct.Struct("@7if2i7q")
+_ATTN_DESC = struct.Struct("@6if3q")
+_CACHE_DESC = struct.Struct("@4q")
+
+
+def _addresses(device, *tensors):
+    """Device addresses; every tensor must be on the call's device (None passes
+    through)."""
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+        elif t.get_device() != device:
+            raise ValueError(f"expected a tensor on the GPU cuda:{device}, got one on {t.device}")
+        else:
+            out.append(t.data_ptr())
+    return out
+
+
+def _device(t) -> int:
+    """Index of the GPU that tensor t is on."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"expected a tensor on the GPU, got one on {t.device}")
+    return d
+
+
+def _row_stride(t, name, width, rows, dtype) -> int:
+    """Row stride of a 2-D tensor of at least `rows` rows of `width` values."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width or shape[0] < rows or t.dtype != dtype:
+        raise ValueError(f"{name}: expected ({rows}, {width}) of {dtype}, got {tuple(shape)} of "
+                         f"{t.dtype}")
+    if shape[0] == 0:
+        return width             # no rows to address
+    stride = t.stride()
+    if stride[1] != 1 and width > 1:
+        raise ValueError(f"{name}: expected a unit stride within a row")
+    # with one row the row stride is never used
+    return stride[0] if shape[0] > 1 else width
+
+
+def _vector(t, name, n, dtype):
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of {n} entries of {dtype}")
+
+
 def _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices, scale,
               qk_l2norm):
-    """Descriptor of a gated delta rule call; the heads follow from the pool's
-    shape (num_slots, HV, DV, DK) and the width of query."""
+    """Packed descriptor of a gated delta rule call; the heads follow from the
+    pool's shape (num_slots, HV, DV, DK) and the width of query."""
     torch = _torch()
-    if state_pool.dim() != 4 or state_pool.dtype != torch.float32 or \
-            not state_pool.is_contiguous():
+    shape = state_pool.shape
+    if len(shape) != 4 or state_pool.dtype != torch.float32 or not state_pool.is_contiguous():
         raise ValueError("state_pool: expected a contiguous float32 (num_slots, HV, DV, DK) "
                          "tensor")
-    _, hv, dv, dk = state_pool.shape
-    strides = [_rows(t, n) for n, t in (("query", query), ("key", key), ("value", value),
-                                        ("a", a), ("b", b), ("out", out))]
-    if dk < 1 or query.shape[1] % dk or query.shape[1] == 0 or key.shape[1] != query.shape[1]:
-        raise ValueError(f"query, key: expected rows of HK * {dk} values")
-    if value.shape[1] != hv * dv or out.shape[1] != hv * dv:
-        raise ValueError(f"value, out: expected rows of {hv} * {dv} values")
-    if a.shape[1] != hv or b.shape[1] != hv:
-        raise ValueError(f"a, b: expected rows of {hv} values")
-    rows = query.shape[0]
-    for name, t in (("key", key), ("value", value), ("a", a), ("b", b), ("out", out)):
-        if t.shape[0] < rows:
-            raise ValueError(f"{name}: {t.shape[0]} rows for {rows} tokens")
-    for name, t in (("key", key), ("value", value), ("out", out)):
-        if t.dtype != query.dtype:
-            raise ValueError(f"{name}: dtype {t.dtype} differs from query's {query.dtype}")
-    if a.dtype != b.dtype:
-        raise ValueError("a, b: expected one dtype")
-    for name, t in (("A_log", A_log), ("dt_bias", dt_bias)):
-        if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != hv:
-            raise ValueError(f"{name}: expected a contiguous float32 tensor of {hv} entries")
-    return sc_gdn_desc(
-        num_k_heads=query.shape[1] // dk, num_v_heads=hv, head_k_dim=dk, head_v_dim=dv,
-        dtype=_dtype_code(query), gate_dtype=_dtype_code(a), qk_l2norm=1 if qk_l2norm else 0,
-        scale=dk ** -0.5 if scale is None else scale, q_row_stride=strides[0],
-        k_row_stride=strides[1], v_row_stride=strides[2], a_row_stride=strides[3],
-        b_row_stride=strides[4], out_row_stride=strides[5],
-        state_indices_stride=_index_stride(state_indices, "state_indices"))
+    _, hv, dv, dk = shape
+    if query.dim() != 2:
+        raise ValueError("query: expected a 2-D tensor")
+    rows, kw = query.shape
+    if dk < 1 or kw % dk or kw == 0:
+        raise ValueError(f"query: expected rows of HK * {dk} values")
+    dtype, gate = query.dtype, a.dtype
+    _vector(A_log, "A_log", hv, torch.float32)
+    _vector(dt_bias, "dt_bias", hv, torch.float32)
+    return _GDN_DESC.pack(
+        kw // dk, hv, dk, dv, _dtype_code(query), _dtype_code(a), 1 if qk_l2norm else 0,
+        dk ** -0.5 if scale is None else scale, _row_stride(query, "query", kw, rows, dtype),
+        _row_stride(key, "key", kw, rows, dtype),
+        _row_stride(value, "value", hv * dv, rows, dtype), _row_stride(a, "a", hv, rows, gate),
+        _row_stride(b, "b", hv, rows, gate), _row_stride(out, "out", hv * dv, rows, dtype),
+        _index_stride(state_indices, "state_indices"))
 
 
 def _workspace(workspace, need, like, stream):
@@ -618,8 +657,8 @@ def _workspace(workspace, need, like, stream):
         workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
         if stream is not None:
             workspace.record_stream(stream)
-    elif workspace.device != like.device or not workspace.is_contiguous():
-        raise ValueError("workspace: expected a contiguous tensor on the call's device")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
     return workspace
 
 
@@ -632,18 +671,16 @@ def sc_gdn_workspace_bytes(num_tokens: int, batch: int, *, num_k_heads: int, num
     """Bytes of workspace that sc_gdn_prefill_varlen needs for a batch of
     `batch` requests with `num_tokens` tokens in all."""
     kw, vw = num_k_heads * head_k_dim, num_v_heads * head_v_dim
-    desc = sc_gdn_desc(num_k_heads=num_k_heads, num_v_heads=num_v_heads, head_k_dim=head_k_dim,
-                       head_v_dim=head_v_dim, dtype=SC_DTYPE_BF16, gate_dtype=SC_DTYPE_BF16,
-                       qk_l2norm=1, scale=1.0, q_row_stride=kw, k_row_stride=kw,
-                       v_row_stride=vw, a_row_stride=num_v_heads, b_row_stride=num_v_heads,
-                       out_row_stride=vw, state_indices_stride=1)
-    return _gdn_need(desc, batch, num_tokens)
+    return _gdn_need(_GDN_DESC.pack(num_k_heads, num_v_heads, head_k_dim, head_v_dim,
+                                    SC_DTYPE_BF16, SC_DTYPE_BF16, 1, 1.0, kw, kw, vw, num_v_heads,
+                                    num_v_heads, vw, 1), batch, num_tokens)
 
 
 def _gdn_need(desc, batch, num_tokens) -> int:
     n = ctypes.c_int64(0)
-    _check("sc_gdn_workspace_bytes",
-           lib().sc_gdn_workspace_bytes(ctypes.byref(desc), batch, num_tokens, ctypes.byref(n)))
+    st = lib().sc_gdn_workspace_bytes(desc, batch, num_tokens, ctypes.byref(n))
+    if st != SC_OK:
+        raise ScError("sc_gdn_workspace_bytes", st)
     return n.value
 
 
@@ -670,14 +707,19 @@ def sc_gdn_prefill_varlen(query, key, value, a, b, A_log, dt_bias, out, state_po
                      scale, qk_l2norm)
     batch, T = query_start_loc.shape[0] - 1, query.shape[0]
     _covers(batch, state_indices=state_indices, has_initial_state=has_initial_state)
+    _flags(has_initial_state, "has_initial_state")
+    dev = _device(query)
     raw = _stream(stream, query)
-    workspace = _workspace(workspace, _gdn_need(desc, batch, T), query, stream)
-    st = lib().sc_gdn_prefill_varlen(
-        ctypes.byref(desc), _ptr(query), _ptr(key), _ptr(value), _ptr(a), _ptr(b), _ptr(A_log),
-        _ptr(dt_bias), _ptr(out), _ptr(state_pool), state_pool.shape[0], _ptr(query_start_loc),
-        _ptr(state_indices), _flags(has_initial_state, "has_initial_state"), batch, T,
-        _ptr(workspace), _nbytes(workspace), raw)
-    _check("sc_gdn_prefill_varlen", st)
+    if workspace is None:
+        workspace = _workspace(None, _gdn_need(desc, batch, T), query, stream)
+    else:
+        _workspace(workspace, 0, query, stream)
+    ptr = _addresses(dev, query, key, value, a, b, A_log, dt_bias, out, state_pool,
+                     query_start_loc, state_indices, has_initial_state, workspace)
+    st = lib().sc_gdn_prefill_varlen(desc, *ptr[:9], state_pool.shape[0], *ptr[9:12], batch, T,
+                                     ptr[12], _nbytes(workspace), raw)
+    if st != SC_OK:
+        raise ScError("sc_gdn_prefill_varlen", st)
 
 
 def sc_gdn_update(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
@@ -691,11 +733,14 @@ def sc_gdn_update(query, key, value, a, b, A_log, dt_bias, out, state_pool, stat
                      scale, qk_l2norm)
     batch = query.shape[0] // q
     _covers(batch, state_indices=state_indices, has_initial_state=has_initial_state)
-    st = lib().sc_gdn_update(
-        ctypes.byref(desc), _ptr(query), _ptr(key), _ptr(value), _ptr(a), _ptr(b), _ptr(A_log),
-        _ptr(dt_bias), _ptr(out), _ptr(state_pool), state_pool.shape[0], _ptr(state_indices),
-        _flags(has_initial_state, "has_initial_state"), batch, q, _stream(stream, query))
-    _check("sc_gdn_update", st)
+    _flags(has_initial_state, "has_initial_state")
+    dev = _device(query)
+    ptr = _addresses(dev, query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
+                     has_initial_state)
+    st = lib().sc_gdn_update(desc, *ptr[:9], state_pool.shape[0], *ptr[9:], batch, q,
+                             _stream(stream, query))
+    if st != SC_OK:
+        raise ScError("sc_gdn_update", st)
 
 
 def sc_gdn_update_spec(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
@@ -714,36 +759,33 @@ def sc_gdn_update_spec(query, key, value, a, b, A_log, dt_bias, out, state_pool,
         raise ValueError("state_indices: expected (B, q) with adjacent entries")
     if num_accepted_tokens.dtype != torch.int32 or not num_accepted_tokens.is_contiguous():
         raise ValueError("num_accepted_tokens: expected a contiguous int32 tensor")
-    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
-                     scale, qk_l2norm)
+    # with at most one row the row stride is never used, and may be anything
+    slots = state_indices if state_indices.shape[0] > 1 else \
+        state_indices.expand(2, -1).as_strided((2, state_indices.shape[1]),
+                                               (state_indices.shape[1], 1))
+    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, slots, scale,
+                     qk_l2norm)
     batch = query.shape[0] // q
-    if batch <= 1:
-        desc.state_indices_stride = state_indices.shape[1]
     _covers(batch, state_indices=state_indices, num_accepted_tokens=num_accepted_tokens)
-    st = lib().sc_gdn_update_spec(
-        ctypes.byref(desc), _ptr(query), _ptr(key), _ptr(value), _ptr(a), _ptr(b), _ptr(A_log),
-        _ptr(dt_bias), _ptr(out), _ptr(state_pool), state_pool.shape[0], _ptr(state_indices),
-        _ptr(num_accepted_tokens), batch, q, _stream(stream, query))
-    _check("sc_gdn_update_spec", st)
+    dev = _device(query)
+    ptr = _addresses(dev, query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
+                     num_accepted_tokens)
+    st = lib().sc_gdn_update_spec(desc, *ptr[:9], state_pool.shape[0], *ptr[9:], batch, q,
+                                  _stream(stream, query))
+    if st != SC_OK:
+        raise ScError("sc_gdn_update_spec", st)
 
 
-def _paged(cache, name, nkv, hd, like):
-    """Descriptor of a (num_blocks, block_size, nkv, hd) cache tensor."""
-    if cache.dim() != 4 or tuple(cache.shape[2:]) != (nkv, hd) or cache.dtype != like.dtype:
-        raise ValueError(f"{name}: expected (num_blocks, block_size, {nkv}, {hd}) of {like.dtype}")
-    if cache.stride(3) != 1:
+def _paged(cache, name, blocks, block_size, nkv, hd, dtype):
+    """Packed descriptor of a (num_blocks, block_size, nkv, hd) cache tensor."""
+    if cache.shape != (blocks, block_size, nkv, hd) or cache.dtype != dtype:
+        raise ValueError(f"{name}: expected ({blocks}, {block_size}, {nkv}, {hd}) of {dtype}")
+    st = cache.stride()
+    if st[3] != 1:
         raise ValueError(f"{name}: expected a unit stride in head_dim")
     # the stride of a dimension of one entry is never used
-    st = [cache.stride(i) if cache.shape[i] > 1 else 0 for i in range(3)]
-    return sc_paged_cache(data=_ptr(cache), block_stride=st[0], token_stride=st[1],
-                          head_stride=st[2])
-
-
-def _int64s(t, name, n):
-    torch = _torch()
-    if t.dtype != torch.int64 or not t.is_contiguous() or t.dim() != 1 or t.shape[0] < n:
-        raise ValueError(f"{name}: expected a contiguous int64 tensor of {n} entries")
-    return _ptr(t)
+    return _CACHE_DESC.pack(cache.data_ptr(), st[0] if blocks > 1 else 0,
+                            st[1] if block_size > 1 else 0, st[2] if nkv > 1 else 0)
 
 
 def sc_qk_norm_rope(query, key, value, q_out, k_out, q_weight, k_weight, cos_sin, positions,
@@ -760,78 +802,60 @@ def sc_qk_norm_rope(query, key, value, q_out, k_out, q_weight, k_weight, cos_sin
     -1 is not written. k_cache, v_cache: (num_blocks, block_size, nkv,
     head_dim), or None for both (value and slots are then not read).
     """
-    T = query.shape[0]
-    if head_dim < 1 or query.shape[1] % head_dim or key.shape[1] % head_dim:
+    torch = _torch()
+    if query.dim() != 2 or key.dim() != 2:
+        raise ValueError("query, key: expected 2-D tensors")
+    T, qw = query.shape
+    kw = key.shape[1]
+    if head_dim < 1 or qw % head_dim or kw % head_dim:
         raise ValueError(f"query, key: expected rows of heads of {head_dim} values")
     if (k_cache is None) != (v_cache is None):
         raise ValueError("k_cache, v_cache: expected both or neither")
-    nq, nkv = query.shape[1] // head_dim, key.shape[1] // head_dim
-    for name, t, w in (("key", key, nkv), ("value", value, nkv), ("q_out", q_out, nq),
-                       ("k_out", k_out, nkv)):
-        if t is None and (name == "k_out" or (name == "value" and k_cache is None)):
-            continue
-        if t.dim() != 2 or t.shape[1] != w * head_dim or t.shape[0] < T or t.dtype != query.dtype:
-            raise ValueError(f"{name}: expected ({T}, {w * head_dim}) of {query.dtype}")
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None and (t.numel() != head_dim or not t.is_contiguous() or
-                              t.dtype != query.dtype):
-            raise ValueError(f"{name}: expected a contiguous tensor of {head_dim} entries of "
-                             f"{query.dtype}")
+    dtype, nkv = query.dtype, kw // head_dim
+    if q_weight is not None:
+        _vector(q_weight, "q_weight", head_dim, dtype)
+    if k_weight is not None:
+        _vector(k_weight, "k_weight", head_dim, dtype)
     kc = vc = None
-    if k_cache is not None:
-        kc = _paged(k_cache, "k_cache", nkv, head_dim, query)
-        vc = _paged(v_cache, "v_cache", nkv, head_dim, query)
-        if k_cache.shape[:2] != v_cache.shape[:2]:
-            raise ValueError("k_cache, v_cache: expected the same blocks")
-    rows = lambda t, n: 0 if t is None else _rows(t, n)
-    desc = sc_qk_norm_desc(
-        num_q_heads=nq, num_kv_heads=nkv, head_dim=head_dim,
-        rotary_dim=0 if cos_sin is None else cos_sin.shape[1],
-        interleaved=1 if interleaved else 0, dtype=_dtype_code(query),
-        table_dtype=SC_DTYPE_F32 if cos_sin is None else _dtype_code(cos_sin), eps=eps,
-        block_size=1 if kc is None else k_cache.shape[1],
-        num_blocks=0 if kc is None else k_cache.shape[0], q_row_stride=_rows(query, "query"),
-        k_row_stride=_rows(key, "key"), v_row_stride=rows(value, "value"),
-        q_out_row_stride=_rows(q_out, "q_out"), k_out_row_stride=rows(k_out, "k_out"),
-        table_row_stride=rows(cos_sin, "cos_sin"),
-        max_position=0 if cos_sin is None else cos_sin.shape[0])
-    st = lib().sc_qk_norm_rope(
-        ctypes.byref(desc), _ptr(query), _ptr(key), None if kc is None else _ptr(value),
-        _ptr(q_out), _ptr(k_out), _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
-        None if cos_sin is None else _int64s(positions, "positions", T),
-        None if kc is None else _int64s(slots, "slots", T),
-        None if kc is None else ctypes.byref(kc), None if vc is None else ctypes.byref(vc), T,
-        _stream(stream, query))
-    _check("sc_qk_norm_rope", st)
-
-
-def _attn_desc(query, out, k_cache, block_table, q, scale):
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
-    blocks, block_size, nkv, hd = k_cache.shape
-    if hd < 1 or query.dim() != 2 or query.shape[1] % hd or query.shape[1] == 0:
-        raise ValueError(f"query: expected rows of heads of {hd} values")
-    if q < 1 or query.shape[0] % q:
-        raise ValueError("rows must be a multiple of q >= 1")
-    if out.dim() != 2 or out.shape[1] != query.shape[1] or out.shape[0] < query.shape[0] or \
-            out.dtype != query.dtype:
-        raise ValueError("out: expected the shape and dtype of query")
-    if block_table.dim() != 2 or block_table.dtype != _torch().int32 or \
-            (block_table.shape[1] > 1 and block_table.numel() and block_table.stride(1) != 1):
-        raise ValueError("block_table: expected int32 (batch, max_blocks) with adjacent entries")
-    return sc_paged_attn_desc(
-        num_q_heads=query.shape[1] // hd, num_kv_heads=nkv, head_dim=hd,
-        dtype=_dtype_code(query), block_size=block_size, num_blocks=blocks,
-        scale=hd ** -0.5 if scale is None else scale, q_row_stride=_rows(query, "query"),
-        out_row_stride=_rows(out, "out"),
-        block_table_row_stride=block_table.stride(0) if block_table.shape[0] > 1
-        else max(block_table.shape[1], 1))
+    v_rs, blocks, block_size = 0, 0, 1
+    if k_cache is None:
+        value = slots = None
+    else:
+        if k_cache.dim() != 4:
+            raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
+        blocks, block_size = k_cache.shape[:2]
+        kc = _paged(k_cache, "k_cache", blocks, block_size, nkv, head_dim, dtype)
+        vc = _paged(v_cache, "v_cache", blocks, block_size, nkv, head_dim, dtype)
+        v_rs = _row_stride(value, "value", kw, T, dtype)
+        if slots.dtype != torch.int64 or slots.dim() != 1 or slots.shape[0] < T or \
+                not slots.is_contiguous():
+            raise ValueError(f"slots: expected a contiguous int64 tensor of {T} entries")
+    rot, t_rs, top, t_code = 0, 0, 0, SC_DTYPE_F32
+    if cos_sin is None:
+        positions = None
+    else:
+        top, rot = cos_sin.shape
+        t_rs, t_code = _row_stride(cos_sin, "cos_sin", rot, top, cos_sin.dtype), _dtype_code(cos_sin)
+        if positions.dtype != torch.int64 or positions.dim() != 1 or positions.shape[0] < T or \
+                not positions.is_contiguous():
+            raise ValueError(f"positions: expected a contiguous int64 tensor of {T} entries")
+    desc = _QK_NORM_DESC.pack(
+        qw // head_dim, nkv, head_dim, rot, 1 if interleaved else 0, _dtype_code(query), t_code,
+        eps, block_size, blocks, _row_stride(query, "query", qw, T, dtype),
+        _row_stride(key, "key", kw, T, dtype), v_rs, _row_stride(q_out, "q_out", qw, T, dtype),
+        0 if k_out is None else _row_stride(k_out, "k_out", kw, T, dtype), t_rs, top)
+    ptr = _addresses(_device(query), query, key, value, q_out, k_out, q_weight, k_weight, cos_sin,
+                     positions, slots, k_cache, v_cache)
+    st = lib().sc_qk_norm_rope(desc, *ptr[:10], kc, vc, T, _stream(stream, query))
+    if st != SC_OK:
+        raise ScError("sc_qk_norm_rope", st)
 
 
 def _attn_need(desc, batch, q, max_seq_len) -> int:
     n = ctypes.c_int64(0)
-    _check("sc_paged_attn_workspace_bytes", lib().sc_paged_attn_workspace_bytes(
-        ctypes.byref(desc), batch, q, max_seq_len, ctypes.byref(n)))
+    st = lib().sc_paged_attn_workspace_bytes(desc, batch, q, max_seq_len, ctypes.byref(n))
+    if st != SC_OK:
+        raise ScError("sc_paged_attn_workspace_bytes", st)
     return n.value
 
 
@@ -840,10 +864,8 @@ def sc_paged_attn_workspace_bytes(batch: int, *, q: int = 1, max_seq_len: int, n
     """Bytes of workspace that sc_paged_attn_decode needs for these sizes on the
     current device (0 where the cache's length is not split)."""
     w = num_q_heads * head_dim
-    return _attn_need(sc_paged_attn_desc(
-        num_q_heads=num_q_heads, num_kv_heads=num_kv_heads, head_dim=head_dim,
-        dtype=SC_DTYPE_BF16, block_size=16, num_blocks=1, scale=1.0, q_row_stride=w,
-        out_row_stride=w, block_table_row_stride=1), batch, q, max_seq_len)
+    return _attn_need(_ATTN_DESC.pack(num_q_heads, num_kv_heads, head_dim, SC_DTYPE_BF16, 16, 1,
+                                      1.0, w, w, 1), batch, q, max_seq_len)
 
 
 def sc_paged_attn_decode(query, out, k_cache, v_cache, block_table, seq_lens, *,
@@ -860,20 +882,42 @@ def sc_paged_attn_decode(query, out, k_cache, v_cache, block_table, seq_lens, *,
     run at the same time).
     """
     torch = _torch()
-    desc = _attn_desc(query, out, k_cache, block_table, q, scale)
-    batch = query.shape[0] // q
-    kc = _paged(k_cache, "k_cache", desc.num_kv_heads, desc.head_dim, query)
-    vc = _paged(v_cache, "v_cache", desc.num_kv_heads, desc.head_dim, query)
-    if k_cache.shape[:2] != v_cache.shape[:2]:
-        raise ValueError("k_cache, v_cache: expected the same blocks")
-    if seq_lens.dtype != torch.int32 or not seq_lens.is_contiguous():
-        raise ValueError("seq_lens: expected a contiguous int32 tensor")
-    _covers(batch, block_table=block_table, seq_lens=seq_lens)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
+    blocks, block_size, nkv, hd = k_cache.shape
+    if query.dim() != 2:
+        raise ValueError("query: expected a 2-D tensor")
+    rows, qw = query.shape
+    if hd < 1 or qw % hd or qw == 0:
+        raise ValueError(f"query: expected rows of heads of {hd} values")
+    if q < 1 or rows % q:
+        raise ValueError("rows must be a multiple of q >= 1")
+    if not 0 <= max_seq_len < 1 << 31:
+        raise ValueError("max_seq_len: expected 0 .. 2^31 - 1")
+    batch, dtype = rows // q, query.dtype
+    table = block_table.shape
+    if len(table) != 2 or table[0] < batch or block_table.dtype != torch.int32:
+        raise ValueError(f"block_table: expected int32 ({batch}, max_blocks)")
+    t_rs, t_cs = block_table.stride()
+    if table[1] > 1 and t_cs != 1 and table[0]:
+        raise ValueError("block_table: expected adjacent entries in a row")
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] < batch or \
+            not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens: expected a contiguous int32 tensor of {batch} entries")
+    desc = _ATTN_DESC.pack(
+        qw // hd, nkv, hd, _dtype_code(query), block_size, blocks,
+        hd ** -0.5 if scale is None else scale, _row_stride(query, "query", qw, rows, dtype),
+        _row_stride(out, "out", qw, rows, dtype), t_rs if table[0] > 1 else max(table[1], 1))
+    kc = _paged(k_cache, "k_cache", blocks, block_size, nkv, hd, dtype)
+    vc = _paged(v_cache, "v_cache", blocks, block_size, nkv, hd, dtype)
+    dev = _device(query)
     raw = _stream(stream, query)
-    need = _attn_need(desc, batch, q, max_seq_len)
-    workspace = _workspace(workspace, need, query, stream)
-    st = lib().sc_paged_attn_decode(
-        ctypes.byref(desc), _ptr(query), _ptr(out), ctypes.byref(kc), ctypes.byref(vc),
-        _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, q, max_seq_len,
-        _ptr(workspace), _nbytes(workspace), raw)
-    _check("sc_paged_attn_decode", st)
+    if workspace is None:
+        workspace = _workspace(None, _attn_need(desc, batch, q, max_seq_len), query, stream)
+    else:
+        _workspace(workspace, 0, query, stream)
+    ptr = _addresses(dev, query, out, block_table, seq_lens, workspace, k_cache, v_cache)
+    st = lib().sc_paged_attn_decode(desc, ptr[0], ptr[1], kc, vc, ptr[2], table[1], ptr[3], batch,
+                                    q, max_seq_len, ptr[4], _nbytes(workspace), raw)
+    if st != SC_OK:
+        raise ScError("sc_paged_attn_decode", st)
