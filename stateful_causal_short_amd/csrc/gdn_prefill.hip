@@ -751,8 +751,11 @@ __global__ __launch_bounds__(64 * (NW + NL)) void gdn_scan(GdnArgs a, int slices
 // of the right-hand sides and of U. Three barriers a chunk: partial products
 // written, right-hand sides written, U written. Left operands are used by one
 // wave each and go straight to registers, a chunk ahead into the other of two
-// sets, in three groups: all at once they fill the address queue, and the wave
-// stands still behind it.
+// sets, in three groups and the first of them between products: all at once
+// they fill the address queue, and the wave stands still behind it (one
+// request of 32,768 tokens: 1.95 ms all at once, 1.19 in groups, 1.09 so). It
+// is still bound by that queue (78 KB a chunk and CU at about 32 bytes a clock)
+// and by the chain; without its loads it takes 0.73 ms.
 // ---------------------------------------------------------------------------
 template <int DK>
 struct KeyFrag;            // DK/4 key dims of a row: a lane's part of a left operand
@@ -916,6 +919,11 @@ __device__ __forceinline__ void scan_few(const GdnArgs& a, FewLds& lds, int r, i
 #pragma unroll
     for (int j = 0; j < 4; ++j) lds.O[w][j][lane] = Q[j];
     load_qk(nxt, cn);
+#pragma unroll
+    for (int i = 0; i < 20; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (i >= 4 && (i & 1)) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
     __syncthreads();
     // 2: right-hand sides v - e^G S k of row tile w
     {
@@ -1054,9 +1062,10 @@ hipError_t launch_dk(const GdnArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((gdn_chunk<DK>), dim3((unsigned)grid), dim3(kBlock), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // Few (request, head, 16 columns): four waves to each. One request of 32,768
-  // tokens, 32 heads x 128: 1.2 ms, and 1.7 ms by the other kernel; eight such
-  // requests of 8,196 tokens in all: 0.34 ms, and 0.20 by the other.
+  // Few (request, head, 16 columns), at most one to a CU: four waves to each.
+  // One request of 32,768 tokens, 32 heads x 128: 1.09 ms, and 1.70 by the
+  // other kernel; eight such requests of 8,196 tokens in all: 0.34 ms, and 0.20
+  // by the other.
   const int64_t tiles = (int64_t)a.batch * a.hv * (a.dv / 16);
   if (tiles <= device_cus()) return launch_few<DK>(a, s);
   return launch_scan<DK, 4, 4>(a, s);
