@@ -443,10 +443,11 @@ sc_status sc_paged_attn_workspace_bytes(const sc_paged_attn_desc* desc, int32_t 
                                         int32_t q_len, int32_t max_seq_len, int64_t* bytes);
 
 /*   block_table (device) int32 (batch, max_blocks): block of each block_size
- *               tokens; entries behind a request's last token are not read; a
- *               block outside the cache holds no visible token
+ *               tokens; entries behind a request's last token may hold
+ *               anything; a block outside the cache holds no visible token
  *   seq_lens    (device) int32 (batch), clamped to [0, max_seq_len]
- *   max_seq_len (host) <= max_blocks * block_size; the split follows from it
+ *   max_seq_len (host) <= max_blocks * block_size and <= 2^30; the split
+ *               follows from it
  *   workspace   (device) 16-byte aligned, or NULL if none is needed; scratch:
  *               calls that may run at once need one each
  * Cache pointers 16-byte aligned, strides a multiple of 8. */

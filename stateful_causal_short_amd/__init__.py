@@ -648,16 +648,19 @@ def _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_in
 
 
 def _workspace(workspace, need, like, stream):
-    """The given workspace, or a new one of `need` bytes from torch's allocator
-    (on the call's stream: freed memory is not reused before the call has run)."""
+    """The given workspace, or a new one of `need` bytes from torch's allocator,
+    in the memory of the stream that the call runs on: a block that another
+    stream has freed may still be in use there, and one freed here is not
+    handed out before the call has run."""
     torch = _torch()
     if workspace is None:
         if need == 0:
             return None
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-        if stream is not None:
-            workspace.record_stream(stream)
-    elif not workspace.is_contiguous():
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=like.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(need, dtype=torch.uint8, device=like.device)
+    if not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
     return workspace
 

@@ -213,8 +213,8 @@ sc_status check_attn_desc(const sc_paged_attn_desc* d) {
 sc_status attn_sizes(const sc_paged_attn_desc* d, int32_t batch, int32_t q_len,
                      int32_t max_seq_len, sc::PagedAttnArgs* a, int64_t* need) {
   if (batch < 0 || q_len < 0 || max_seq_len < 0) return SC_ERR_INVALID_ARG;
-  // rows, row groups and splits are counted with 32 bits
-  if ((int64_t)batch * q_len * d->num_q_heads > 0x7FFFFFFFLL || max_seq_len > 0x7FFF0000)
+  // rows, row groups and the ends of splits are counted with 32 bits
+  if ((int64_t)batch * q_len * d->num_q_heads > 0x7FFFFFFFLL || max_seq_len > (1 << 30))
     return SC_ERR_UNSUPPORTED;
   *a = sc::PagedAttnArgs{};
   *need = 0;

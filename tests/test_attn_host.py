@@ -108,6 +108,7 @@ def test_attn_descriptor_refusals(kw, status):
     (dict(kc=cache(data=0x50008)), UNSUPPORTED), (dict(vc=cache(head_stride=12)), UNSUPPORTED),
     (dict(q=ODD), UNSUPPORTED), (dict(out=ODD), UNSUPPORTED),
     (dict(batch=0, q=None, kc=None), OK), (dict(n=0, q=None), OK),
+    (dict(top=(1 << 30) + 1), UNSUPPORTED),
 ])
 def test_attn_refusals(kw, status):
     assert attn(attn_desc(), **kw) == status
@@ -171,6 +172,13 @@ def test_attn_binding_refuses(change):
         t["seq_lens"] = t["seq_lens"].long()
     with pytest.raises(ValueError):
         scs.sc_paged_attn_decode(*t.values(), max_seq_len=64, q=q)
+
+
+@pytest.mark.parametrize("top", [-1, 1 << 31, (1 << 32) + 5])
+def test_attn_binding_refuses_lengths_that_do_not_fit(top):
+    _, t = attn_tensors()
+    with pytest.raises(ValueError):
+        scs.sc_paged_attn_decode(*t.values(), max_seq_len=top)
 
 
 @pytest.mark.parametrize("change", ["head_dim", "one_cache", "value", "q_out", "k_out", "weight",

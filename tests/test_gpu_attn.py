@@ -309,6 +309,22 @@ def test_lengths_are_clamped():
     assert bool((out[1] == 0).all())
 
 
+def test_empty_calls():
+    print("[gpu] attn empty calls", flush=True)
+    S = scs()
+    kc = torch.zeros(2, 16, 1, 64, dtype=BF16, device="cuda")
+    out = torch.full((2, 64), 7.5, dtype=BF16, device="cuda")
+    q = torch.ones(2, 64, dtype=BF16, device="cuda")
+    none = torch.zeros(0, 4, dtype=torch.int32, device="cuda")
+    S.sc_paged_attn_decode(q[:0], out[:0], kc, kc, none, i32([]), max_seq_len=64)
+    S.sc_qk_norm_rope(q[:0], q[:0], q[:0], out[:0], None, None, None, None, None, i64([]), kc, kc,
+                      head_dim=64)
+    torch.cuda.synchronize()
+    assert bool((out == 7.5).all()) and bool((kc == 0).all())
+    S.sc_paged_attn_decode(q, out, kc, kc, none.new_zeros(2, 4), i32([0, 0]), max_seq_len=0)
+    assert bool((out == 0).all())
+
+
 @pytest.mark.parametrize("hd,value", [(64, float("nan")), (128, float("inf")), (256, float("-inf"))])
 def test_later_drafts_do_not_reach_earlier_ones(hd, value):
     """A non-finite value row of draft j is in the results of drafts >= j alone."""

@@ -344,6 +344,67 @@ def test_other_stream_and_given_workspace():
                                 workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
 
 
+def test_workspace_belongs_to_the_stream_of_the_call():
+    """A block that the current stream has freed but still writes to is not the
+    workspace of a call on another stream."""
+    hk, hv, dk, dv, T = 2, 4, 128, 128, 640
+    c = G.make(hk, hv, dk, dv, T, 3, seed=14)
+    d = gpu(c)
+    print("[gpu] gdn workspace of a side stream", flush=True)
+    S = scs()
+    need = S.sc_gdn_workspace_bytes(T, 1, num_k_heads=hk, num_v_heads=hv, head_k_dim=dk,
+                                    head_v_dim=dv)
+    has = torch.tensor([1], dtype=torch.uint8, device="cuda")
+    qsl, idx = i32([0, T]), i32([1])
+    want, pool = sentinel(T, hv * dv), d["pool"].clone()
+    S.sc_gdn_prefill_varlen(*call_args(d, want, pool), qsl, idx, has)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    out, pool2 = sentinel(T, hv * dv), d["pool"].clone()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        junk = torch.empty(need, dtype=torch.uint8, device="cuda")
+        for _ in range(200):
+            junk.fill_(0xFF)
+        del junk                                         # freed, and still being written
+        pool2.copy_(d["pool"])
+        side.wait_stream(torch.cuda.current_stream())
+        junk = torch.empty(need, dtype=torch.uint8, device="cuda")
+        for _ in range(200):
+            junk.fill_(0xFF)
+        del junk
+        S.sc_gdn_prefill_varlen(*call_args(d, out, pool2), qsl, idx, has, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(pool2, pool)
+
+
+def test_zero_rows_and_no_pool():
+    """Empty batches are no-ops; without slots every request starts from zeros."""
+    hk, hv, dk, dv = 1, 2, 64, 32
+    c = G.make(hk, hv, dk, dv, 70, 1, seed=15)
+    d = gpu(c)
+    print("[gpu] gdn empty calls", flush=True)
+    S = scs()
+    none = torch.empty(0, hv, dv, dk, device="cuda")
+    out = sentinel(70, hv * dv)
+    has = torch.ones(1, dtype=torch.uint8, device="cuda")
+    S.sc_gdn_update(*call_args(d, out, none, slice(0, 0)), i32([]))
+    S.sc_gdn_prefill_varlen(*call_args(d, out, none, slice(0, 0)), i32([0]), i32([]), has[:0])
+    S.sc_gdn_prefill_varlen(*call_args(d, out, none, slice(0, 0)), i32([0, 0]), i32([0]), has)
+    torch.cuda.synchronize()
+    assert bool((out == 7.5).all())
+    zero = torch.zeros(hv, dv, dk, dtype=G.F64)
+    S.sc_gdn_prefill_varlen(*call_args(d, out, none, slice(0, 68)), i32([0, 68]), i32([0]), has)
+    S.sc_gdn_update(*call_args(d, out, none, slice(68, 70)), i32([0]), q=2)
+    for rows in (range(68), range(68, 70)):
+        want, _, bd = G.reference(c, rows, zero, dk ** -0.5)
+        bound = torch.stack(bd)
+        bound = torch.maximum(bound, bound.amax(dim=(0, 2), keepdim=True))
+        G.check_out(out.cpu()[list(rows)].view(len(rows), hv, dv), torch.stack(want), bound,
+                    len(rows), dk)
+
+
 def test_conv_then_delta_rule():
     """The two steps of such a layer together: the mixed-qkv conv, then the
     delta rule on column blocks of its output, for a prefill that continues one
