@@ -427,7 +427,20 @@ typedef __attribute__((address_space(3))) void* lptr;
 struct ScanWork {
   int r, h, slice, row_lo, rows, base, nch;
 };
-__device__ __forceinline__ ScanWork scan_work(const GdnArgs& a, int slices) {
+// The i-th longest request (of up to 64; else request i): a scan takes as long
+// as its chunks, so where workgroups wait for a CU the longest go first.
+__device__ __forceinline__ int by_length(const GdnArgs& a, int i) {
+  if (a.batch > 64) return i;
+  const int lane = (int)(threadIdx.x & 63);
+  const int n = lane < a.batch ? a.qsl[lane + 1] - a.qsl[lane] : -1;
+  int rank = 0;
+  for (int m = 0; m < a.batch; ++m) {
+    const int o = __builtin_amdgcn_readlane(n, m);
+    rank += o > n || (o == n && m < lane) ? 1 : 0;
+  }
+  return __ffsll(__ballot(lane < a.batch && rank == i)) - 1;
+}
+__device__ __forceinline__ ScanWork scan_work(const GdnArgs& a, int slices, bool sorted) {
   ScanWork k{};
   const int rep = a.hv / a.hk;
   const unsigned per_group = (unsigned)(rep * slices);
@@ -438,6 +451,7 @@ __device__ __forceinline__ ScanWork scan_work(const GdnArgs& a, int slices) {
   k.slice = (int)(in_group % (unsigned)slices);
   k.h = (int)(group % (unsigned)a.hk) * rep + (int)(in_group / (unsigned)slices);
   k.r = (int)(group / (unsigned)a.hk);
+  if (sorted) k.r = by_length(a, k.r);
   const int T = (int)a.num_tokens;
   const int s0 = __builtin_amdgcn_readfirstlane(a.qsl[k.r]);
   const int s1 = __builtin_amdgcn_readfirstlane(a.qsl[k.r + 1]);
@@ -456,7 +470,7 @@ __global__ __launch_bounds__(64 * (NW + NL)) void gdn_scan(GdnArgs a, int slices
   constexpr int KS = DK / 32;
   __shared__ __align__(16) char first[2][B::kFirst];
   __shared__ __align__(16) char second[B::kSecond];
-  const ScanWork wk = scan_work(a, slices);
+  const ScanWork wk = scan_work(a, slices, true);
   const int r = wk.r, h = wk.h, slice = wk.slice, row_lo = wk.row_lo, rows = wk.rows;
   const int base = wk.base, nch = wk.nch, hk = h / (a.hv / a.hk);
   if (nch <= 0) return;                       // no tokens: the slot stays as it is
@@ -487,10 +501,8 @@ __global__ __launch_bounds__(64 * (NW + NL)) void gdn_scan(GdnArgs a, int slices
     constexpr int VR = 2 * NW;
     const int vt = lane / VR, vrun = lane % VR;
     const uint16_t* const vb = (const uint16_t*)a.v + row_lo * a.v_rs + h * a.dv;
-    auto load_first = [&](int c) {
+    auto load_rows = [&](int c) {
       char* const dst = first[c & 1];
-      const char* const ws = wsb + (int64_t)c * a.hv * GdnWorkspace::kHead;
-      const int64_t r0 = (int64_t)c * CH;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t row = min(c * CH + j * 16 + l16, rows - 1);
@@ -502,17 +514,22 @@ __global__ __launch_bounds__(64 * (NW + NL)) void gdn_scan(GdnArgs a, int slices
           put(qb + row * a.q_rs + ks * 32, dst + B::kQ + (j * KS + ks) * B::kF);
         }
       }
+    };
+    auto load_rest = [&](int c) {
+      char* const dst = first[c & 1];
+      const char* const ws = wsb + (int64_t)c * a.hv * GdnWorkspace::kHead;
       put_run(ws + GdnWorkspace::kT + GdnWorkspace::kP, dst + B::kVec, GdnWorkspace::kVec);
 #pragma unroll
       for (int tb = 0; tb < CH; tb += NL * (64 / VR)) {
         const int t0 = tb + ld * (64 / VR), t = t0 + vt;
         const int run = (vrun - 2 * ((t >> 2) & 3)) & (VR - 1);
         const int col = min((slice * NW) * 16 + run * 8, a.dv - 8);   // behind the last: unused
-        put(vb + min(r0 + t, (int64_t)rows - 1) * a.v_rs + col, dst + B::kV + t0 * NW * 32);
+        put(vb + (int64_t)min(c * CH + t, rows - 1) * a.v_rs + col, dst + B::kV + t0 * NW * 32);
       }
       put_run(ws, dst + B::kT, GdnWorkspace::kT);
     };
-    load_first(0);
+    load_rows(0);
+    load_rest(0);
     for (int c = 0; c < nch; ++c) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();                     // first half of c is there; the second buffer is free
@@ -521,7 +538,10 @@ __global__ __launch_bounds__(64 * (NW + NL)) void gdn_scan(GdnArgs a, int slices
       put_run(ws + GdnWorkspace::kT, second + B::kP, GdnWorkspace::kP);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();                     // second half of c is there
-      if (c + 1 < nch) load_first(c + 1);
+      if (c + 1 < nch) {
+        load_rows(c + 1);
+        load_rest(c + 1);
+      }
     }
     return;
   }
@@ -1025,7 +1045,7 @@ __device__ __forceinline__ void scan_few(const GdnArgs& a, FewLds& lds, int r, i
 template <int DK>
 __global__ __launch_bounds__(kBlock) void gdn_scan_few(GdnArgs a) {
   __shared__ FewLds lds;
-  const ScanWork k = scan_work(a, a.dv / 16);
+  const ScanWork k = scan_work(a, a.dv / 16, false);
   if (k.nch <= 0) return;                     // no tokens: the slot stays as it is
   const int lane = (int)(threadIdx.x & 63);
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
