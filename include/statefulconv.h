@@ -309,7 +309,8 @@ sc_status sc_cca_qk_conv(const sc_cca_desc* desc, const void* q, const void* k,
  *   a, b    (T, num_v_heads), gate_dtype; A_log, dt_bias (num_v_heads) fp32
  *   state   (num_slots, num_v_heads, DV, DK) fp32, contiguous, 16-byte aligned
  * DK is 64 or 128, DV a multiple of 16 (SC_ERR_UNSUPPORTED otherwise; also
- * for rows that break the alignment above). */
+ * for rows that break the alignment above). `out` overlaps no input; two
+ * requests of a call share no slot. */
 typedef struct {
   int32_t num_k_heads;   /* HK >= 1 */
   int32_t num_v_heads;   /* HV, a multiple of HK */
@@ -424,8 +425,9 @@ sc_status sc_qk_norm_rope(const sc_qk_norm_desc* desc, const void* q, const void
  * seq_lens[r] tokens, the new ones last, so new token j sees positions
  * [0, seq_lens[r] - q_len + j]. Query head h reads key/value head
  * h / (num_q_heads / num_kv_heads).
- *   out = sum_t softmax_t(scale q.k_t) v_t;  a row that sees nothing: zeros
- * Scores, weights and sums are fp32. */
+ *   out = sum_t softmax_t(scale q.k_t) v_t
+ * A row that sees nothing, or only scores of minus infinity, is zeros. Scores,
+ * weights and sums are fp32. `out` overlaps no input. */
 typedef struct {
   int32_t num_q_heads, num_kv_heads;
   int32_t head_dim;        /* 64, 128 or 256 (SC_ERR_UNSUPPORTED otherwise) */

@@ -620,7 +620,7 @@ def _vector(t, name, n, dtype):
         raise ValueError(f"{name}: expected a contiguous tensor of {n} entries of {dtype}")
 
 
-def _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices, scale,
+def _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, index_stride, scale,
               qk_l2norm):
     """Packed descriptor of a gated delta rule call; the heads follow from the
     pool's shape (num_slots, HV, DV, DK) and the width of query."""
@@ -644,7 +644,7 @@ def _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_in
         _row_stride(key, "key", kw, rows, dtype),
         _row_stride(value, "value", hv * dv, rows, dtype), _row_stride(a, "a", hv, rows, gate),
         _row_stride(b, "b", hv, rows, gate), _row_stride(out, "out", hv * dv, rows, dtype),
-        _index_stride(state_indices, "state_indices"))
+        index_stride)
 
 
 def _workspace(workspace, need, like, stream):
@@ -706,8 +706,8 @@ def sc_gdn_prefill_varlen(query, key, value, a, b, A_log, dt_bias, out, state_po
             query_start_loc.dim() != 1 or query_start_loc.shape[0] < 1:
         raise ValueError("query_start_loc: expected a contiguous int32 tensor of batch + 1 "
                          "entries")
-    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
-                     scale, qk_l2norm)
+    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool,
+                     _index_stride(state_indices, "state_indices"), scale, qk_l2norm)
     batch, T = query_start_loc.shape[0] - 1, query.shape[0]
     _covers(batch, state_indices=state_indices, has_initial_state=has_initial_state)
     _flags(has_initial_state, "has_initial_state")
@@ -732,8 +732,8 @@ def sc_gdn_update(query, key, value, a, b, A_log, dt_bias, out, state_pool, stat
     updates ``state_pool`` in place. Tensors as for sc_gdn_prefill_varlen."""
     if q < 1 or query.shape[0] % q:
         raise ValueError("rows must be a multiple of q >= 1")
-    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, state_indices,
-                     scale, qk_l2norm)
+    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool,
+                     _index_stride(state_indices, "state_indices"), scale, qk_l2norm)
     batch = query.shape[0] // q
     _covers(batch, state_indices=state_indices, has_initial_state=has_initial_state)
     _flags(has_initial_state, "has_initial_state")
@@ -762,11 +762,10 @@ def sc_gdn_update_spec(query, key, value, a, b, A_log, dt_bias, out, state_pool,
         raise ValueError("state_indices: expected (B, q) with adjacent entries")
     if num_accepted_tokens.dtype != torch.int32 or not num_accepted_tokens.is_contiguous():
         raise ValueError("num_accepted_tokens: expected a contiguous int32 tensor")
-    # with at most one row the row stride is never used, and may be anything
-    slots = state_indices if state_indices.shape[0] > 1 else \
-        state_indices.expand(2, -1).as_strided((2, state_indices.shape[1]),
-                                               (state_indices.shape[1], 1))
-    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, slots, scale,
+    stride = _index_stride(state_indices, "state_indices")
+    if state_indices.shape[0] <= 1:
+        stride = state_indices.shape[1]      # never used; the library wants a row's length
+    desc = _gdn_desc(query, key, value, a, b, A_log, dt_bias, out, state_pool, stride, scale,
                      qk_l2norm)
     batch = query.shape[0] // q
     _covers(batch, state_indices=state_indices, num_accepted_tokens=num_accepted_tokens)

@@ -157,3 +157,14 @@ def test_binding_refuses_host_tensors_and_short_slot_rows():
     t["state_indices"] = torch.zeros(3, 4, dtype=torch.int32)[:, ::2]
     with pytest.raises(ValueError):
         scs.sc_gdn_update_spec(*t.values(), acc, q=2)       # slots not adjacent
+
+
+def test_binding_takes_empty_speculative_batches():
+    """No requests: the slots are (0, q), whatever their strides; the only thing
+    wrong with this call is where its tensors are."""
+    torch, t = tensors()
+    for name in ("query", "key", "value", "a", "b", "out"):
+        t[name] = t[name][:0]
+    t["state_indices"] = torch.zeros(0, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="on the GPU"):
+        scs.sc_gdn_update_spec(*t.values(), torch.zeros(0, dtype=torch.int32), q=2)

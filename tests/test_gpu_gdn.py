@@ -405,6 +405,32 @@ def test_zero_rows_and_no_pool():
                     len(rows), dk)
 
 
+def test_empty_speculative_batch_and_slots_of_2d_columns():
+    """A speculative call of no requests is a no-op; prefill and updates take
+    their slots from column 0 of a 2-D array."""
+    hk, hv, dk, dv = 1, 2, 64, 32
+    c = G.make(hk, hv, dk, dv, 9, 6, seed=16)
+    d = gpu(c)
+    print("[gpu] gdn 2-D slots", flush=True)
+    S = scs()
+    out, pool = sentinel(9, hv * dv), d["pool"].clone()
+    S.sc_gdn_update_spec(*call_args(d, out, pool, slice(0, 0)), i32([]).view(0, 3), i32([]), q=3)
+    torch.cuda.synchronize()
+    assert bool((out == 7.5).all()) and torch.equal(pool, d["pool"])
+    wide = i32([[4, 0, 0], [1, 0, 0], [2, 0, 0]])
+    has = torch.ones(3, dtype=torch.uint8, device="cuda")
+    for slots in (wide, wide[:, 0].contiguous()):
+        got, p = sentinel(9, hv * dv), d["pool"].clone()
+        S.sc_gdn_prefill_varlen(*call_args(d, got, p, slice(0, 9)), i32([0, 4, 5, 9]), slots, has)
+        again, p2 = sentinel(9, hv * dv), d["pool"].clone()
+        S.sc_gdn_update(*call_args(d, again, p2, slice(0, 9)), slots, q=3)
+        if slots is wide:
+            kept = (got, p, again, p2)
+    for x, y in zip(kept, (got, p, again, p2)):
+        assert torch.equal(x, y)
+    assert not torch.equal(kept[1], d["pool"]) and torch.equal(kept[1][[0, 3, 5]], d["pool"][[0, 3, 5]])
+
+
 def test_conv_then_delta_rule():
     """The two steps of such a layer together: the mixed-qkv conv, then the
     delta rule on column blocks of its output, for a prefill that continues one
