@@ -6,7 +6,10 @@
  * token batches, optionally dilated, with bias and SiLU, whose per-request
  * history of the last (width-1)*dilation raw inputs lives in a slot-indexed
  * state pool; plus the CCA variant (depthwise then per-head grouped conv, a
- * residual mix and a one-token-delayed value).
+ * residual mix and a one-token-delayed value). And the operators that take the
+ * convs' outputs: the gated delta rule on a pool of matrix states, and for CCA
+ * the head norms with rotation and cache write and the attention of new tokens
+ * over that paged cache.
  *
  * Defining passages (page title, section):
  *  - "vllm.model_executor.layers.mamba.ops.cpu.gdn_attention":

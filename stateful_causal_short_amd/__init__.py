@@ -1,4 +1,6 @@
-"""MI355X (gfx950) stateful causal short convolution.
+"""MI355X (gfx950) stateful causal short convolution, and the operators that
+take its outputs: the gated delta rule (prefill, update, speculative update),
+head norms with rotation and cache write, and paged decode attention.
 
 Thin Python binding of ``libstatefulconv.so`` (C ABI in
 ``include/statefulconv.h``). Every function here only marshals arguments —
