@@ -42,7 +42,7 @@ struct PagedAttnArgs {
   int64_t q_rs, out_rs, table_rs;
   float scale;
   int32_t batch, nq_tok, nq, nkv, hd, block_size, num_blocks, max_len;
-  int32_t splits, split_len; // set by plan_paged_attn
+  int32_t splits, split_len, sorted; // set by plan_paged_attn
 };
 
 // Splits of the cache's length and the workspace they need (bytes).

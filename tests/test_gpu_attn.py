@@ -276,6 +276,40 @@ def test_paged_attention(case):
     assert torch.equal(again[:-1], out[:-1])
 
 
+MANY = [  # nq, nkv, hd, q, requests, lengths: more workgroups than the card holds at once
+    (8, 4, 64, 1, 400, "some"),        # taken by falling length
+    (4, 4, 64, 1, 512, "equal"),       # ... with all of them in one step
+    (8, 4, 64, 1, 513, "some"),        # one more than are put in order
+    (16, 4, 128, 2, 70, "long"),       # ... and with the length split
+    (4, 2, 256, 1, 300, "one"),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=[f"{c[1]}x{c[2]}-{c[4]}-{c[5]}" for c in MANY])
+def test_paged_attention_many_requests(case):
+    """Each request has its rows, whatever the order in which they are taken."""
+    nq, nkv, hd, q, B, kind = case
+    print(f"[gpu] attn many {case}", flush=True)
+    g = torch.Generator().manual_seed(B)
+    rng = np.random.default_rng(B)
+    lens = {"some": rng.integers(0, 90, B), "equal": np.full(B, 33),
+            "long": np.where(np.arange(B) % 9 == 4, rng.integers(2000, 3300, B),
+                             rng.integers(0, 40, B)),
+            "one": np.where(np.arange(B) == 250, 129, 1)}[kind].tolist()
+    kc, vc, table, k, v = paged(g, lens, nkv, hd, 16, "tokens", rng)
+    query = randn(g, B * q, nq * hd)
+    out = torch.full((B * q + 1, nq * hd), 7.5, dtype=BF16, device="cuda")
+    call = dict(q=q, max_seq_len=max(lens))
+    scs().sc_paged_attn_decode(query.cuda(), out[:-1], kc, vc, i32(table), i32(lens), **call)
+    want, tol = attn_ref(query, k, v, lens, q, hd ** -0.5)
+    got = out.cpu()
+    check_attn(got[:-1].view(B * q, nq, hd), want.view(B * q, nq, hd), tol.view(B * q, nq, hd))
+    assert bool((got[-1] == 7.5).all())
+    again = torch.zeros_like(out)
+    scs().sc_paged_attn_decode(query.cuda(), again[:-1], kc, vc, i32(table), i32(lens), **call)
+    assert torch.equal(again[:-1].cpu(), got[:-1])
+
+
 def test_pages_outside_the_cache_hold_no_token():
     """A table entry outside the cache: its tokens are as if they were absent."""
     nq, nkv, hd, block = 4, 2, 64, 16
