@@ -574,7 +574,7 @@ sc_status sc_gdn_workspace_bytes(const sc_gdn_desc* desc, int32_t batch, int64_t
   *bytes = batch == 0 || num_tokens == 0
                ? 0
                : sc::GdnWorkspace::bytes(gdn_chunks(batch, num_tokens), desc->num_k_heads,
-                                         desc->num_v_heads, desc->head_k_dim);
+                                         desc->num_v_heads, desc->head_k_dim, batch);
   return SC_OK;
 }
 
@@ -601,7 +601,7 @@ sc_status sc_gdn_prefill_varlen(const sc_gdn_desc* desc, const void* q, const vo
   const int64_t chunks = gdn_chunks(batch, num_tokens);
   if (chunks > 0x7FFFFFFFLL) return SC_ERR_UNSUPPORTED;
   if (!al16(workspace) ||
-      workspace_bytes < sc::GdnWorkspace::bytes(chunks, g.hk, g.hv, g.dk))
+      workspace_bytes < sc::GdnWorkspace::bytes(chunks, g.hk, g.hv, g.dk, batch))
     return SC_ERR_INVALID_ARG;
   g.qsl = query_start_loc;
   g.has_init = has_initial_state;

@@ -31,11 +31,13 @@ struct GdnArgs {
   int32_t hk, hv, dk, dv, l2norm, gate_f32, num_slots, batch;
   int32_t nq;                // update: tokens per request
   int32_t n_chunks;          // prefill: chunk slots of the workspace
+  int32_t sorted;            // prefill: the scan takes requests in the workspace's order
 };
 
 // Prefill workspace: for each (chunk, value head) the matrices T and P of the
 // chunk as MFMA operands (16-bit parts, 3 of T and 2 of P), and its row
-// factors; for each (chunk, key head) the keys transposed.
+// factors; for each (chunk, key head) the keys transposed; last, the requests by
+// falling length.
 struct GdnWorkspace {
   static constexpr int64_t kFrag = 1024;             // 64 lanes x 16 bytes
   static constexpr int64_t kFrags = 6;               // (row tile, k step) pairs at or below the diagonal
@@ -44,8 +46,11 @@ struct GdnWorkspace {
   static constexpr int64_t kDecay = 3 * kGdnChunk * 4;
   static constexpr int64_t kVec = 4 * kGdnChunk * 4; // three row factors, the chunk's decay
   static constexpr int64_t kHead = kT + kP + kVec;
-  static int64_t bytes(int64_t n_chunks, int64_t hk, int64_t hv, int64_t dk) {
+  __host__ __device__ static int64_t order(int64_t n_chunks, int64_t hk, int64_t hv, int64_t dk) {
     return n_chunks * (hv * kHead + hk * dk * kGdnChunk * 2);
+  }
+  static int64_t bytes(int64_t n_chunks, int64_t hk, int64_t hv, int64_t dk, int64_t batch) {
+    return order(n_chunks, hk, hv, dk) + batch * 4;
   }
 };
 

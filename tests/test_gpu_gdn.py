@@ -128,6 +128,11 @@ PREFILLS = [  # hk, hv, dk, dv, lengths, gates, strong, pad
     (8, 16, 64, 80, [65, 2, 0, 190] + [7] * 20, "f32", True, 8),
     (2, 4, 128, 16, [1, 70, 64] * 24, "bf16", False, 0),
     (4, 12, 64, 128, [100, 33, 1], "bf16", True, 16),
+    # many requests, taken by falling length, equal and empty ones among them;
+    # then more than are put in order
+    (1, 1, 64, 16, [3, 1, 0, 7, 1, 1, 70] * 40 + [200, 0], "bf16", False, 0),
+    (1, 2, 64, 32, [1] * 65 + [129] + [2] * 9, "f32", False, 0),
+    (1, 1, 64, 16, [1] * 1000 + [0, 90] + [2] * 38, "bf16", False, 0),
 ]
 
 
