@@ -78,7 +78,9 @@ __device__ __forceinline__ void split8(f32x4 a, f32x4 b, u32x4* part) {
 
 // Range-checked buffer over the n rows (<= 64, of stride rs elements) from p:
 // rows behind them read zeros and drop stores. The base is uniform, so a
-// lane's offsets within a chunk stay the same from chunk to chunk.
+// lane's offsets within a chunk stay the same from chunk to chunk. The check
+// covers the lane's own (vector) offset; the scalar offset of the builtins is
+// outside it by their contract, so a row's distance always goes into the former.
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 __device__ __forceinline__ rsrc_t make_rsrc(const void* p, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
@@ -811,15 +813,15 @@ struct KeyFrag;            // DK/4 key dims of a row: a lane's part of a left op
 template <>
 struct KeyFrag<128> {
   u32x4 x;
-  __device__ __forceinline__ void load(rsrc_t r, uint32_t off, uint32_t soff) {
-    x = __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0);
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t off) {
+    x = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
   }
 };
 template <>
 struct KeyFrag<64> {
   u32x2 x;
-  __device__ __forceinline__ void load(rsrc_t r, uint32_t off, uint32_t soff) {
-    x = __builtin_amdgcn_raw_buffer_load_b64(r, off, soff, 0);
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t off) {
+    x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
   }
 };
 __device__ __forceinline__ f32x4 mfma_key(const KeyFrag<128>& a, const KeyFrag<128>& b, f32x4 c) {
@@ -904,14 +906,14 @@ __device__ __forceinline__ void scan_few(const GdnArgs& a, FewLds& lds, int r, i
     const rsrc_t qr = row_rsrc(qb + (int64_t)c * CH * a.q_rs, a.q_rs, n);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      o.k[j].load(kr, k_off, j * 16 * krs);
-      o.q[j].load(qr, q_off, j * 16 * qrs);
+      o.k[j].load(kr, k_off + j * 16 * krs);
+      o.q[j].load(qr, q_off + j * 16 * qrs);
     }
   };
   auto load_t = [&](Ops& o, int c) {
     const rsrc_t vr = row_rsrc(vb + (int64_t)c * CH * a.v_rs, a.v_rs, min(rows - c * CH, CH));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o.v[i] = __builtin_amdgcn_raw_buffer_load_b16(vr, v_off, i * vrs, 0);
+    for (int i = 0; i < 4; ++i) o.v[i] = __builtin_amdgcn_raw_buffer_load_b16(vr, v_off + i * vrs, 0, 0);
     const rsrc_t m = matrices(c);
     o.c_rhs = ld_factor(m, 0);
     o.c_upd = ld_factor(m, 1);
