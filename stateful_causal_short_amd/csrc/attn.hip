@@ -91,9 +91,12 @@ __device__ __forceinline__ int by_length(const PagedAttnArgs& a, int i) {
   return at;
 }
 
+// Workspace: the maximum and the sum of each (query row, split), then, 16-byte
+// aligned, its hd values. The float at which those begin, for n of them:
+__host__ __device__ inline int64_t values_at(int64_t n) { return (n * 2 + 3) & ~(int64_t)3; }
+
 }  // namespace
 
-// Workspace: for each (query row, split) the maximum, the sum and hd values.
 template <int HD>
 __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAttnArgs a) {
   constexpr int KS = HD / 32;               // score products per tile
@@ -314,7 +317,7 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
   }
   const float inv = a.splits > 1 ? 1.f : (lt > 0.f ? 1.f / lt : 0.f);
   const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
-  float* const wo = a.ws + n_rows * a.splits * 2;
+  float* const wo = a.ws + values_at(n_rows * a.splits);
   const int64_t part = (q_row * a.nq + head) * a.splits + split;
   if (a.splits > 1 && row_ok && lg == 0) {
     a.ws[part * 2] = mt;
@@ -367,7 +370,7 @@ __global__ __launch_bounds__(kBlock) void attn_join(PagedAttnArgs a) {
   const int len = min(max(a.lens[r], 0), a.max_len);
   const int n = max(1, min(a.splits, (len + a.split_len - 1) / a.split_len));
   const float* ml = a.ws + row * a.splits * 2;
-  const float* part = a.ws + n_rows * a.splits * 2 + row * a.splits * HD + lane * N;
+  const float* part = a.ws + values_at(n_rows * a.splits) + row * a.splits * HD + lane * N;
   const float mine = lane < n ? ml[lane * 2] : kNone;
   float lt = lane < n ? ml[lane * 2 + 1] : 0.f;
   float y[N];
@@ -424,7 +427,8 @@ int64_t plan_paged_attn(PagedAttnArgs* a) {
   a->sorted = base * splits > 4 * cus && a->batch > 1 && a->batch <= kSortMax;
   a->split_len = (int32_t)(per * unit);
   if (splits == 1) return 0;
-  return (int64_t)a->batch * a->nq_tok * a->nq * splits * (a->hd + 2) * (int64_t)sizeof(float);
+  const int64_t parts = (int64_t)a->batch * a->nq_tok * a->nq * splits;
+  return (values_at(parts) + parts * a->hd) * (int64_t)sizeof(float);
 }
 
 namespace {

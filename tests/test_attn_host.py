@@ -210,3 +210,14 @@ def test_norm_binding_refuses(change):
         t["v_cache"] = z(9, 16, 2, 128)
     with pytest.raises(ValueError):
         scs.sc_qk_norm_rope(*t.values(), head_dim=hd)
+
+
+@pytest.mark.parametrize("nq,nkv,hd,batch,q,top", [(7, 1, 128, 1, 1, 3500), (3, 3, 64, 5, 1, 2300),
+                                                   (1, 1, 256, 1, 1, 1400), (8, 2, 128, 2, 2, 4096)])
+def test_attn_parts_are_whole_vectors(nq, nkv, hd, batch, q, top):
+    """The parts of the splits are stored 16 bytes at a time, behind two floats
+    for each: they begin at a multiple of 16 bytes, so that the workspace, parts
+    of 4 hd bytes behind it, has whole vectors too."""
+    need = scs.sc_paged_attn_workspace_bytes(batch, q=q, max_seq_len=top, num_q_heads=nq,
+                                             num_kv_heads=nkv, head_dim=hd)
+    assert need > 0 and need % 16 == 0
