@@ -565,12 +565,6 @@ def sc_cca_qk_conv(q, k, v_cur, v_del, out, w_dw, b_dw, w_gr, b_gr, delayed_init
     _check("sc_cca_qk_conv", st)
 
 
-__all__ = ["lib", "ScError", "LIB_PATH", "EXPORTS", "sc_conv_desc", "sc_ckpt_desc",
-           "sc_cca_desc", "sc_conv_fuse", "sc_conv_prefill_varlen", "sc_conv_update",
-           "sc_conv_update_spec", "sc_conv_update_spec_varlen", "sc_validate_metadata",
-           "sc_state_gather", "sc_state_scatter", "sc_cca_qk_conv"]
-
-
 # The calls below marshal a dozen small things each, and a decode step is as
 # long as its marshalling: descriptors are packed as bytes (the layout of the
 # structures above), and each tensor's shape and strides are read once.
@@ -925,3 +919,12 @@ def sc_paged_attn_decode(query, out, k_cache, v_cache, block_table, seq_lens, *,
                                     q, max_seq_len, ptr[4], _nbytes(workspace), raw)
     if st != SC_OK:
         raise ScError("sc_paged_attn_decode", st)
+
+
+__all__ = ["lib", "ScError", "LIB_PATH", "EXPORTS", "sc_conv_desc", "sc_ckpt_desc",
+           "sc_cca_desc", "sc_conv_fuse", "sc_gdn_desc", "sc_qk_norm_desc", "sc_paged_cache",
+           "sc_paged_attn_desc", "sc_conv_prefill_varlen", "sc_conv_update",
+           "sc_conv_update_spec", "sc_conv_update_spec_varlen", "sc_validate_metadata",
+           "sc_state_gather", "sc_state_scatter", "sc_cca_qk_conv", "sc_gdn_workspace_bytes",
+           "sc_gdn_prefill_varlen", "sc_gdn_update", "sc_gdn_update_spec", "sc_qk_norm_rope",
+           "sc_paged_attn_workspace_bytes", "sc_paged_attn_decode"]
