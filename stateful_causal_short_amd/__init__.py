@@ -566,12 +566,18 @@ def sc_cca_qk_conv(q, k, v_cur, v_del, out, w_dw, b_dw, w_gr, b_gr, delayed_init
 
 
 # The calls below marshal a dozen small things each, and a decode step is as
-# long as its marshalling: descriptors are packed as bytes (the layout of the
-# structures above), and each tensor's shape and strides are read once.
-_GDN_DESC = struct.Struct("@7if7q")
-_QK_NORM_DESC = struct.Struct("@7if2i7q")
-_ATTN_DESC = struct.Struct("@6if3q")
-_CACHE_DESC = struct.Struct("@4q")
+# long as its marshalling: descriptors are packed as bytes, in the layout of the
+# structures above, and each tensor's shape and strides are read once.
+def _packer(structure) -> struct.Struct:
+    codes = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P"}
+    # native alignment, the end included ("0q")
+    return struct.Struct("@" + "".join(codes[t] for _, t in structure._fields_) + "0q")
+
+
+_GDN_DESC = _packer(sc_gdn_desc)
+_QK_NORM_DESC = _packer(sc_qk_norm_desc)
+_ATTN_DESC = _packer(sc_paged_attn_desc)
+_CACHE_DESC = _packer(sc_paged_cache)
 
 
 def _addresses(device, *tensors):
