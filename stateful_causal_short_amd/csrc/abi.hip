@@ -133,8 +133,13 @@ sc_status check_gdn_desc(const sc_gdn_desc* d) {
   return SC_OK;
 }
 
-int64_t gdn_chunks(int32_t batch, int64_t num_tokens) {
-  return num_tokens / sc::kGdnChunk + batch;
+// Chunks of a prefill; SC_ERR_UNSUPPORTED where its launches do not fit.
+sc_status gdn_chunks(const sc_gdn_desc* d, int32_t batch, int64_t num_tokens, int64_t* chunks) {
+  if (num_tokens > 0x7FFFFFFFLL) return SC_ERR_UNSUPPORTED;
+  *chunks = num_tokens / sc::kGdnChunk + batch;
+  return sc::gdn_prefill_fits(*chunks, batch, d->num_k_heads, d->num_v_heads, d->head_v_dim)
+             ? SC_OK
+             : SC_ERR_UNSUPPORTED;
 }
 
 // Pointers and sizes common to the three calls.
@@ -570,11 +575,12 @@ sc_status sc_gdn_workspace_bytes(const sc_gdn_desc* desc, int32_t batch, int64_t
   sc_status st = check_gdn_desc(desc);
   if (st != SC_OK) return st;
   if (batch < 0 || num_tokens < 0) return SC_ERR_INVALID_ARG;
-  if (num_tokens > 0x7FFFFFFFLL) return SC_ERR_UNSUPPORTED;
+  int64_t chunks = 0;
+  if ((st = gdn_chunks(desc, batch, num_tokens, &chunks)) != SC_OK) return st;
   *bytes = batch == 0 || num_tokens == 0
                ? 0
-               : sc::GdnWorkspace::bytes(gdn_chunks(batch, num_tokens), desc->num_k_heads,
-                                         desc->num_v_heads, desc->head_k_dim, batch);
+               : sc::GdnWorkspace::bytes(chunks, desc->num_k_heads, desc->num_v_heads,
+                                         desc->head_k_dim, batch);
   return SC_OK;
 }
 
@@ -592,14 +598,13 @@ sc_status sc_gdn_prefill_varlen(const sc_gdn_desc* desc, const void* q, const vo
   if (batch < 0 || num_tokens < 0 || num_slots < 0 || workspace_bytes < 0)
     return SC_ERR_INVALID_ARG;
   if (batch == 0 || num_tokens == 0) return SC_OK;
-  if (num_tokens > 0x7FFFFFFFLL) return SC_ERR_UNSUPPORTED;
+  int64_t chunks = 0;
+  if ((st = gdn_chunks(desc, batch, num_tokens, &chunks)) != SC_OK) return st;
   if (!query_start_loc || !has_initial_state || !workspace) return SC_ERR_NULL_ARG;
   sc::GdnArgs g;
   st = gdn_args(desc, q, k, v, a, b, A_log, dt_bias, out, state_pool, num_slots, state_indices,
                 batch, &g);
   if (st != SC_OK) return st;
-  const int64_t chunks = gdn_chunks(batch, num_tokens);
-  if (chunks > 0x7FFFFFFFLL) return SC_ERR_UNSUPPORTED;
   if (!al16(workspace) ||
       workspace_bytes < sc::GdnWorkspace::bytes(chunks, g.hk, g.hv, g.dk, batch))
     return SC_ERR_INVALID_ARG;

@@ -54,6 +54,9 @@ struct GdnWorkspace {
   }
 };
 
+// Whether the grids of a prefill can be launched (and its workspace counted).
+bool gdn_prefill_fits(int64_t n_chunks, int64_t batch, int64_t hk, int64_t hv, int64_t dv);
+
 hipError_t launch_gdn_update(const GdnArgs& a, hipStream_t stream);
 hipError_t launch_gdn_prefill(const GdnArgs& a, hipStream_t stream);
 

@@ -1087,21 +1087,26 @@ __global__ __launch_bounds__(kBlock) void gdn_scan_few(GdnArgs a) {
 }
 
 namespace {
-template <int DK, int NW, int NL>
+constexpr int kScanWaves = 4;      // compute waves of gdn_scan, and as many loaders
+
+// Workgroups of a scan that takes `width` value columns in each.
+int64_t scan_grid(int64_t batch, int64_t hk, int64_t hv, int64_t dv, int width) {
+  const int64_t groups = (batch * hk + kXcds - 1) / kXcds * kXcds;
+  return groups * (hv / hk) * ((dv + width - 1) / width);
+}
+
+template <int DK>
 hipError_t launch_scan(const GdnArgs& a, hipStream_t s) {
-  const int slices = (a.dv + 16 * NW - 1) / (16 * NW);
-  const int64_t groups = ((int64_t)a.batch * a.hk + kXcds - 1) / kXcds * kXcds;
-  const int64_t grid = groups * (a.hv / a.hk) * slices;
-  if (grid > 0x7FFFFFFFLL) return hipErrorNotSupported;
-  hipLaunchKernelGGL((gdn_scan<DK, NW, NL>), dim3((unsigned)grid), dim3(64 * (NW + NL)), 0, s, a, slices);
+  constexpr int NW = kScanWaves, NL = kScanWaves;
+  const int64_t grid = scan_grid(a.batch, a.hk, a.hv, a.dv, 16 * NW);
+  hipLaunchKernelGGL((gdn_scan<DK, NW, NL>), dim3((unsigned)grid), dim3(64 * (NW + NL)), 0, s, a,
+                     (a.dv + 16 * NW - 1) / (16 * NW));
   return hipGetLastError();
 }
 
 template <int DK>
 hipError_t launch_few(const GdnArgs& a, hipStream_t s) {
-  const int64_t groups = ((int64_t)a.batch * a.hk + kXcds - 1) / kXcds * kXcds;
-  const int64_t grid = groups * (a.hv / a.hk) * (a.dv / 16);
-  if (grid > 0x7FFFFFFFLL) return hipErrorNotSupported;
+  const int64_t grid = scan_grid(a.batch, a.hk, a.hv, a.dv, 16);
   hipLaunchKernelGGL((gdn_scan_few<DK>), dim3((unsigned)grid), dim3(kBlock), 0, s, a);
   return hipGetLastError();
 }
@@ -1112,7 +1117,6 @@ hipError_t launch_dk(GdnArgs a, hipStream_t s) {
   const bool few = tiles <= device_cus();
   a.sorted = !few && a.batch > 1 && a.batch <= kSortMax;
   const int64_t grid = (int64_t)a.n_chunks * a.hv + a.sorted;
-  if (grid > 0x7FFFFFFFLL) return hipErrorNotSupported;
   hipLaunchKernelGGL((gdn_chunk<DK>), dim3((unsigned)grid), dim3(kBlock), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -1121,9 +1125,16 @@ hipError_t launch_dk(GdnArgs a, hipStream_t s) {
   // other kernel; eight such requests of 8,196 tokens in all: 0.34 ms, and 0.16
   // to 0.20 by the other.
   if (few) return launch_few<DK>(a, s);
-  return launch_scan<DK, 4, 4>(a, s);
+  return launch_scan<DK>(a, s);
 }
 }  // namespace
+
+// Of the scans' grids only that of many columns can be too large: the other is
+// for at most one workgroup a CU.
+bool gdn_prefill_fits(int64_t n_chunks, int64_t batch, int64_t hk, int64_t hv, int64_t dv) {
+  return n_chunks <= (0x7FFFFFFFLL - 1) / hv &&
+         scan_grid(batch, hk, hv, dv, 16 * kScanWaves) <= 0x7FFFFFFFLL;
+}
 
 hipError_t launch_gdn_prefill(const GdnArgs& a, hipStream_t s) {
   if (a.dk == 128) return launch_dk<128>(a, s);

@@ -168,3 +168,19 @@ def test_binding_takes_empty_speculative_batches():
     t["state_indices"] = torch.zeros(0, 2, dtype=torch.int32)
     with pytest.raises(ValueError, match="on the GPU"):
         scs.sc_gdn_update_spec(*t.values(), torch.zeros(0, dtype=torch.int32), q=2)
+
+
+def test_sizes_that_cannot_be_launched_are_refused_before_a_launch():
+    """More workgroups than a grid holds, in the first launch or only in the
+    second; the bytes of such a workspace may not fit 64 bits either."""
+    n = ctypes.c_int64(-7)
+    many = desc(num_k_heads=1, num_v_heads=1 << 19, head_v_dim=16, v_row_stride=1 << 23,
+                out_row_stride=1 << 23, a_row_stride=1 << 19, b_row_stride=1 << 19)
+    assert scs.lib().sc_gdn_workspace_bytes(ctypes.byref(many), (1 << 31) - 1, (1 << 31) - 1,
+                                            ctypes.byref(n)) == UNSUPPORTED
+    wide = desc(num_k_heads=1, num_v_heads=1, head_v_dim=1 << 22, v_row_stride=1 << 22,
+                out_row_stride=1 << 22)
+    assert scs.lib().sc_gdn_workspace_bytes(ctypes.byref(wide), 1 << 15, 1,
+                                            ctypes.byref(n)) == UNSUPPORTED
+    assert prefill(wide, batch=1 << 15, T=1) == UNSUPPORTED
+    assert n.value == -7
