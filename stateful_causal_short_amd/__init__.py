@@ -667,6 +667,13 @@ def _workspace(workspace, need, like, stream):
     return workspace
 
 
+def _fits(bits, **sizes):
+    """Sizes that no tensor bounds: the call's C integers would cut them."""
+    for name, n in sizes.items():
+        if not -(1 << bits - 1) <= n < 1 << bits - 1:
+            raise ValueError(f"{name}: {n} does not fit {bits} bits")
+
+
 def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -675,6 +682,8 @@ def sc_gdn_workspace_bytes(num_tokens: int, batch: int, *, num_k_heads: int, num
                            head_k_dim: int, head_v_dim: int) -> int:
     """Bytes of workspace that sc_gdn_prefill_varlen needs for a batch of
     `batch` requests with `num_tokens` tokens in all."""
+    _fits(32, batch=batch)
+    _fits(64, num_tokens=num_tokens)
     kw, vw = num_k_heads * head_k_dim, num_v_heads * head_v_dim
     return _gdn_need(_GDN_DESC.pack(num_k_heads, num_v_heads, head_k_dim, head_v_dim,
                                     SC_DTYPE_BF16, SC_DTYPE_BF16, 1, 1.0, kw, kw, vw, num_v_heads,
@@ -867,6 +876,7 @@ def sc_paged_attn_workspace_bytes(batch: int, *, q: int = 1, max_seq_len: int, n
                                   num_kv_heads: int, head_dim: int) -> int:
     """Bytes of workspace that sc_paged_attn_decode needs for these sizes on the
     current device (0 where the cache's length is not split)."""
+    _fits(32, batch=batch, q=q, max_seq_len=max_seq_len)
     w = num_q_heads * head_dim
     return _attn_need(_ATTN_DESC.pack(num_q_heads, num_kv_heads, head_dim, SC_DTYPE_BF16, 16, 1,
                                       1.0, w, w, 1), batch, q, max_seq_len)

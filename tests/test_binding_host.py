@@ -27,3 +27,19 @@ def test_packed_descriptors_have_the_layout_of_the_structures(packer, structure)
     values = range(3, 3 + len(structure._fields_))
     d = structure.from_buffer_copy(pack.pack(*values))
     assert [getattr(d, name) for name, _ in structure._fields_] == list(values)
+
+
+@pytest.mark.parametrize("sizes", [dict(batch=(1 << 32) + 1), dict(q=(1 << 32) + 1),
+                                   dict(max_seq_len=(1 << 32) + 64), dict(max_seq_len=1 << 31)])
+def test_attention_workspace_sizes_are_not_cut(sizes):
+    call = dict(batch=1, q=1, max_seq_len=64)
+    call.update(sizes)
+    with pytest.raises(ValueError):
+        scs.sc_paged_attn_workspace_bytes(**call, num_q_heads=4, num_kv_heads=2, head_dim=128)
+
+
+@pytest.mark.parametrize("tokens,batch", [(64, (1 << 32) + 1), (64, 1 << 31), ((1 << 64) + 64, 1)])
+def test_delta_rule_workspace_sizes_are_not_cut(tokens, batch):
+    with pytest.raises(ValueError):
+        scs.sc_gdn_workspace_bytes(tokens, batch, num_k_heads=2, num_v_heads=4, head_k_dim=128,
+                                   head_v_dim=64)
