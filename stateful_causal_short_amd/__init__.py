@@ -216,6 +216,9 @@ def _stream(stream, like=None) -> Optional[int]:
         raise ValueError(f"tensors are on cuda:{like.get_device()} but the current device is "
                          f"cuda:{cur}; call under torch.cuda.device({like.get_device()})")
     if stream is not None:
+        if getattr(stream, "device_index", cur) != cur:
+            raise ValueError(f"the stream is on cuda:{stream.device_index} but the current device "
+                             f"is cuda:{cur}")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(cur)
 

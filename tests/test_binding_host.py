@@ -1,5 +1,6 @@
 """What the binding offers and how it packs its arguments, without a GPU."""
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 
@@ -43,3 +44,14 @@ def test_delta_rule_workspace_sizes_are_not_cut(tokens, batch):
     with pytest.raises(ValueError):
         scs.sc_gdn_workspace_bytes(tokens, batch, num_k_heads=2, num_v_heads=4, head_k_dim=128,
                                    head_v_dim=64)
+
+
+def test_streams_of_another_device_are_refused(monkeypatch):
+    """The kernels run on the current device, and so must their stream."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    tensor = SimpleNamespace(is_cuda=True, get_device=lambda: 1)
+    here, there = (SimpleNamespace(cuda_stream=77, device_index=i) for i in (1, 0))
+    assert scs._stream(here, tensor) == 77
+    with pytest.raises(ValueError, match="cuda:0"):
+        scs._stream(there, tensor)
