@@ -430,7 +430,8 @@ sc_status sc_qk_norm_rope(const sc_qk_norm_desc* desc, const void* q, const void
  * h / (num_q_heads / num_kv_heads).
  *   out = sum_t softmax_t(scale q.k_t) v_t
  * A row that sees nothing, or only scores of minus infinity, is zeros. Scores,
- * weights and sums are fp32. `out` overlaps no input. */
+ * weights and sums are fp32, the scores in base 2: one of a size above 2.3e38
+ * counts as infinite. `out` overlaps no input. */
 typedef struct {
   int32_t num_q_heads, num_kv_heads;
   int32_t head_dim;        /* 64, 128 or 256 (SC_ERR_UNSUPPORTED otherwise) */
