@@ -839,6 +839,8 @@ def sc_qk_norm_rope(query, key, value, q_out, k_out, q_weight, k_weight, cos_sin
     else:
         if k_cache.dim() != 4:
             raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
+        if value is None or slots is None:
+            raise ValueError("value, slots: expected with the caches")
         blocks, block_size = k_cache.shape[:2]
         kc = _paged(k_cache, "k_cache", blocks, block_size, nkv, head_dim, dtype)
         vc = _paged(v_cache, "v_cache", blocks, block_size, nkv, head_dim, dtype)
@@ -852,8 +854,8 @@ def sc_qk_norm_rope(query, key, value, q_out, k_out, q_weight, k_weight, cos_sin
     else:
         top, rot = cos_sin.shape
         t_rs, t_code = _row_stride(cos_sin, "cos_sin", rot, top, cos_sin.dtype), _dtype_code(cos_sin)
-        if positions.dtype != torch.int64 or positions.dim() != 1 or positions.shape[0] < T or \
-                not positions.is_contiguous():
+        if positions is None or positions.dtype != torch.int64 or positions.dim() != 1 or \
+                positions.shape[0] < T or not positions.is_contiguous():
             raise ValueError(f"positions: expected a contiguous int64 tensor of {T} entries")
     desc = _QK_NORM_DESC.pack(
         qw // head_dim, nkv, head_dim, rot, 1 if interleaved else 0, _dtype_code(query), t_code,

@@ -221,3 +221,17 @@ def test_attn_parts_are_whole_vectors(nq, nkv, hd, batch, q, top):
     need = scs.sc_paged_attn_workspace_bytes(batch, q=q, max_seq_len=top, num_q_heads=nq,
                                              num_kv_heads=nkv, head_dim=hd)
     assert need > 0 and need % 16 == 0
+
+
+@pytest.mark.parametrize("missing", ["value", "slots", "positions"])
+def test_norm_binding_names_what_is_missing(missing):
+    """value and slots belong to the caches, positions to the table."""
+    torch = pytest.importorskip("torch")
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    t = dict(query=z(4, 512), key=z(4, 256), value=z(4, 256), q_out=z(4, 512), k_out=None,
+             q_weight=None, k_weight=None, cos_sin=torch.zeros(9, 64),
+             positions=torch.zeros(4, dtype=torch.int64), slots=torch.zeros(4, dtype=torch.int64),
+             k_cache=z(8, 16, 2, 128), v_cache=z(8, 16, 2, 128))
+    t[missing] = None
+    with pytest.raises(ValueError, match=missing):
+        scs.sc_qk_norm_rope(*t.values(), head_dim=128)
