@@ -420,11 +420,16 @@ int64_t plan_paged_attn(PagedAttnArgs* a) {
   const int64_t per = (units + splits - 1) / splits;
   splits = (units + per - 1) / per;
   a->splits = (int32_t)splits;
-  // Where workgroups wait for a CU (each holds four), the longest requests go
-  // first and the last to start are short: 512 requests of up to 2,048 tokens
-  // 233 us as they come, 208 so; 64 x 4 drafts 127-130, 116-129. Where none
-  // waits, finding the order is 1.2 us of 10.5 for nothing.
-  a->sorted = base * splits > 4 * cus && a->batch > 1 && a->batch <= kSortMax;
+  // Where workgroups wait for a CU, the longest requests go first and the last to
+  // start are short. As they come / so, 16 query and 4 key/value heads x 128: 512
+  // requests of up to 2,048 tokens 233 / 208 us, 1,000 tokens 123 / 110, 400 tokens
+  // 55 / 55, 200 tokens 27 / 32 and 100 tokens 20 / 25, where each workgroup's look
+  // at all lengths outweighs it; 400 x 4 drafts of up to 1,000 tokens 136 / 129; 64 x 4
+  // of up to 8,192 127-130 / 116-129. Hence 512 tokens or more. With 1,000 requests, twice
+  // the lengths to look at, 2,048 tokens 422 / 398 and 200 tokens 54 / 74: kSortMax
+  // stays at 512. A CU holds four workgroups, or two of 256-wide heads; the order
+  // made no difference between two and four there (300 requests x 2 heads, 146 us).
+  a->sorted = base * splits > 4 * cus && a->batch > 1 && a->batch <= kSortMax && a->max_len >= 512;
   a->split_len = (int32_t)(per * unit);
   if (splits == 1) return 0;
   const int64_t parts = (int64_t)a->batch * a->nq_tok * a->nq * splits;

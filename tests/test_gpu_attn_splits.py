@@ -1,5 +1,6 @@
-"""Attention over a split cache on the GPU, where rows and splits are odd in
-number, in a workspace of exactly the bytes that are asked for."""
+"""Attention on the GPU over a split cache, where rows and splits are odd in
+number, in a workspace of exactly the bytes that are asked for; and of requests
+that are taken by falling length."""
 import numpy as np
 import pytest
 
@@ -35,3 +36,35 @@ def test_odd_parts(case):
     want, tol = attn_ref(query, k, v, lens, q, hd ** -0.5)
     check_attn(out.cpu(), want, tol)
     assert bool((room[need:] == 0xFF).all())
+
+
+ORDERED = [  # nq, nkv, hd, q, requests, lengths; max_seq_len of 512 and more
+    (8, 4, 64, 1, 400, "some"),
+    (4, 4, 64, 1, 512, "equal"),
+    (8, 4, 64, 1, 513, "some"),        # one more than are put in order
+    (4, 2, 256, 1, 300, "one"),
+    (16, 4, 128, 2, 70, "none"),
+]
+
+
+@pytest.mark.parametrize("top", [512, 700])
+@pytest.mark.parametrize("case", ORDERED, ids=[f"{c[1]}x{c[2]}-{c[4]}-{c[5]}" for c in ORDERED])
+def test_requests_in_order(case, top):
+    """Each request has its rows, whatever the order in which they are taken."""
+    nq, nkv, hd, q, B, kind = case
+    print(f"[gpu] attn ordered {case} {top}", flush=True)
+    g = torch.Generator().manual_seed(B)
+    rng = np.random.default_rng(B)
+    lens = {"some": rng.integers(0, 90, B), "equal": np.full(B, 33),
+            "one": np.where(np.arange(B) == 250, 129, 1), "none": np.zeros(B, int)}[kind].tolist()
+    kc, vc, table, k, v = paged(g, lens, nkv, hd, 16, "tokens", rng)
+    wide = np.full((B, 44), 10 ** 9)                       # 704 tokens; not read behind the end
+    wide[:, :table.shape[1]] = table
+    query = randn(g, B * q, nq * hd)
+    out = torch.full((B * q + 1, nq * hd), 7.5, dtype=BF16, device="cuda")
+    scs().sc_paged_attn_decode(query.cuda(), out[:-1], kc, vc, i32(wide), i32(lens), q=q,
+                               max_seq_len=top)
+    want, tol = attn_ref(query, k, v, lens, q, hd ** -0.5)
+    got = out.cpu()
+    check_attn(got[:-1].view(B * q, nq, hd), want.view(B * q, nq, hd), tol.view(B * q, nq, hd))
+    assert bool((got[-1] == 7.5).all())
