@@ -295,16 +295,17 @@ sc_status sc_cca_qk_conv(const sc_cca_desc* desc, const void* q, const void* k,
                          int64_t num_tokens, void* stream);
 
 /* Gated delta rule (GDN page "vllm.model_executor.layers.mamba.ops.cpu.
- * gdn_attention": the recurrence that consumes the mixed-qkv conv's output, as
- * decode, speculative decode and varlen prefill, with the gates computed from
- * A_log, a, b and dt_bias). Per value head, with a state S (DV x DK) that lives
- * in a slot pool next to the conv state:
+ * gdn_attention": it hands the mixed-qkv conv's output to this recurrence, as
+ * decode, speculative decode and varlen prefill, with gates from A_log, a, b and
+ * dt_bias; the arithmetic is not on the page, and is the rule's usual one). Per
+ * value head, with a state S (DV x DK) that lives in a slot pool next to the
+ * conv state:
  *   g = -exp(A_log) * softplus(a + dt_bias),  beta = sigmoid(b)
  *   q^, k^ = q, k scaled by 1/sqrt(sum of squares + 1e-6) (qk_l2norm = 1), or as they are
  *   S <- exp(g) S;  S <- S + beta (v - S k^) k^T;  out = scale * S q^
  * Value head h reads key head h / (num_v_heads / num_k_heads). q, k, v and out
  * are bf16 (the page's core rejects other inputs); the state, the gates and
- * every sum are fp32.
+ * every sum are fp32, whose range a head's sum of squares must not pass.
  *   q, k    (T, num_k_heads * DK), v, out (T, num_v_heads * DV): rows of their
  *           strides, e.g. the column blocks of the conv's output rows; q, k and
  *           v 16-byte aligned with strides a multiple of 8, out 8-byte
@@ -380,14 +381,16 @@ typedef struct {
   int64_t block_stride, token_stride, head_stride;
 } sc_paged_cache;
 
-/* Norms of query and key heads, position rotation and cache write (ZAYA page:
- * what its attention does with the [query | key | value] rows of
- * ZayaCCA.project before it attends). Per head x of head_dim values:
+/* Norms of query and key heads, position rotation and cache write, for the
+ * [query | key | value] rows that sc_cca_qk_conv writes. The four pages end
+ * before this step: these are the usual root-mean-square norm and rotation, not
+ * a form that they print. Per head x of head_dim values, all heads with one weight:
  *   x^ = weight * x / sqrt(mean(x^2) + eps)           (weight NULL: 1)
  *   pair i of the first rotary_dim values turns by the table's angle i:
  *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin), the pair being values
  *   (i, i + rotary_dim/2), or (2i, 2i + 1) with interleaved = 1
- * in fp32 with one rounding at the store. Values are copied. */
+ * in fp32 with one rounding at the store (a head whose sum of squares passes
+ * fp32's range, from values near 2^60 on, comes out as zeros). Values are copied. */
 typedef struct {
   int32_t num_q_heads, num_kv_heads;
   int32_t head_dim;        /* 64, 128 or 256 (SC_ERR_UNSUPPORTED otherwise) */
@@ -423,7 +426,8 @@ sc_status sc_qk_norm_rope(const sc_qk_norm_desc* desc, const void* q, const void
                           const sc_paged_cache* v_cache, int64_t num_tokens, void* stream);
 
 /* Attention of the newest tokens over a paged cache (the attention that reads
- * what sc_qk_norm_rope wrote). `batch` requests of exactly q_len new tokens,
+ * what sc_qk_norm_rope wrote; the usual softmax form, as none of the pages prints
+ * it). `batch` requests of exactly q_len new tokens,
  * request r owning rows [r*q_len, (r+1)*q_len) of q and out; its cache holds
  * seq_lens[r] tokens, the new ones last, so new token j sees positions
  * [0, seq_lens[r] - q_len + j]. Query head h reads key/value head

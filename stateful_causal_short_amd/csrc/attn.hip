@@ -2,11 +2,13 @@
 //
 //   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t - max)
 //
-// over the positions a token sees. The bytes of the cache bound it: keys and
-// values are read once from HBM straight into registers, as MFMA operands.
+// over the positions a token sees. The bytes of the cache bound it: a group of
+// up to 16 rows (the query heads of one key/value head, times the request's new
+// tokens) reads keys and values once from HBM straight into registers, as MFMA
+// operands. More rows are more groups, in workgroups of their own, and each
+// reads the cache again.
 //
-// A group of up to 16 rows (the query heads of one key/value head, times the
-// request's new tokens) shares each key: scores of 16 cached tokens x 16 rows
+// The rows of a group share each key: scores of 16 cached tokens x 16 rows
 // are one 16x16x32 bf16 product per 32 values of a head, with the keys as the
 // left operand as they lie in the cache. A score tile then has row n = lane %
 // 16 and tokens 4 (lane / 16) + i in register i, which is how the fp32
@@ -23,8 +25,8 @@
 // tokens 155 + 7 us (805 MB, 5.2 TB/s in the first); 512 requests of up to
 // 2,048 tokens 208 us (1,078 MB, 5.2 TB/s; 5.5 with even lengths); 64 x 4 drafts
 // over up to 8,192 tokens 116-135 + 9 us, where uneven splits and the start and
-// end of each workgroup show; one request of 300 tokens 10.5 us, the latency of
-// length -> page -> key -> softmax -> join.
+// end of each workgroup show; one request of 300 tokens 10.8 us: a wave's five
+// tiles in turn, each page -> key -> softmax -> values, on four CUs, and the join.
 #include "attn.hpp"
 #include "common.hpp"
 
@@ -355,7 +357,8 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
 }
 
 // Adds the splits of a query row: a workgroup per row, its waves take splits in
-// turn (all loads of a wave in flight together), hd/64 values a lane.
+// turn, hd/64 values a lane. Up to 16 loads one after another in a wave: 7 us for
+// 64 splits of 48 rows, 9 us for 16 of 4,096.
 template <int HD>
 __global__ __launch_bounds__(kBlock) void attn_join(PagedAttnArgs a) {
   constexpr int N = HD / 64;
@@ -383,7 +386,6 @@ __global__ __launch_bounds__(kBlock) void attn_join(PagedAttnArgs a) {
   lt *= f;
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) lt += __shfl_xor(lt, d);
-#pragma unroll 4
   for (int s = w; s < n; s += 4) {
     const float fs = __shfl(f, s);
 #pragma unroll
@@ -412,8 +414,9 @@ int64_t plan_paged_attn(PagedAttnArgs* a) {
   const int64_t units = std::max<int64_t>(1, (a->max_len + unit - 1) / unit);
   // Eight workgroups a CU, or sixteen where they come from the split alone
   // (lengths differ, and a short request's splits end at once: 64 x 4 drafts
-  // over up to 8,192 tokens took 159 us with eight, 140 with sixteen or more);
-  // a split has 512 tokens or more.
+  // over up to 8,192 tokens took 159 us with eight, 140 with sixteen or more).
+  // Not more than one for each 512 tokens or part of them: a length just above
+  // 512 is two splits of 320.
   const int64_t cus = device_cus(), want = base >= 4 * cus ? 8 * cus : 16 * cus;
   int64_t splits = std::min<int64_t>({(want + base - 1) / base, (units + 7) / 8, kMaxSplits});
   splits = std::max<int64_t>(splits, 1);

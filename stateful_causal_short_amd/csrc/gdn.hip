@@ -166,7 +166,11 @@ hipError_t launch_dk(const GdnArgs& a, hipStream_t s) {
   // x 128 x 128, plain / streaming: 16 requests 15.3 / 17.3 us, 64 48.5 / 49.9,
   // 128 104.8 / 98.2, 512 389 / 369 (5.9 TB/s). Speculative updates write a
   // state for each draft and read one: 128 x 4 took 235 us, 255 streaming.
-  // Plain stores instead: 412 us at 512 requests, 271 at 128 x 4.
+  // Streaming stores for R = 8, which starts at 16 requests of 32 heads; streaming
+  // / plain, over 1 GB of states in all, as a model's layers have: 16 requests
+  // 18.8 / 19.5 us, 24 20.9 / 26.6, 32 25.3 / 33.6, 64 49.2 / 51.8, 128 97.5 /
+  // 107.7, 512 389 / 412; 16 x 4 drafts 31.1 / 42.6, 128 x 4 230 / 272. Over two
+  // sets of states, which the last level keeps, 24 to 64 requests lose 2 to 8%.
   if (pairs * a.dv * DK * 4 >= (int64_t)128 << 20) return launch_r<DK, 8, true>(a, s);
   return launch_r<DK, 8, false>(a, s);
 }

@@ -14,9 +14,10 @@
 // Precision: the state and every sum are fp32. Products run on bf16 MFMA with
 // each fp32 factor cut into 16-bit parts (x = hi + mid + lo to 2^-24) and
 // the small cross terms left out; q, k and v enter as they are, which is
-// exact: the unit lengths of q and k are row factors applied in fp32. P and
-// the copy of U it multiplies carry two parts (2^-16): their product only
-// reaches the bf16 output.
+// exact: the unit lengths of q and k are row factors applied in fp32. P, the
+// copy of U it multiplies and the state as Q multiplies it carry two parts (they
+// leave 2^-16): those products only reach the bf16 output, whose own rounding is
+// 2^-8 of a value. The gates are fp32, their running sum in a chunk fp64.
 #include "conv_device.hpp"
 #include "gdn_device.hpp"
 
@@ -804,7 +805,7 @@ __global__ __launch_bounds__(64 * (NW + NL)) void gdn_scan(GdnArgs a, int slices
 // wave each and go straight to registers, a chunk ahead into the other of two
 // sets, in three groups and the first of them between products: all at once
 // they fill the address queue, and the wave stands still behind it (one
-// request of 32,768 tokens: 1.95 ms all at once, 1.19 in groups, 1.09 so). It
+// request of 32,768 tokens: 1.95 ms all at once, 1.19 in groups, 1.10 so). It
 // is still bound by that queue (78 KB a chunk and CU at about 32 bytes a clock)
 // and by the chain; without its loads it takes 0.73 ms.
 // ---------------------------------------------------------------------------
@@ -1121,7 +1122,7 @@ hipError_t launch_dk(GdnArgs a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // Few (request, head, 16 columns), at most one to a CU: four waves to each.
-  // One request of 32,768 tokens, 32 heads x 128: 1.09 ms, and 1.70 by the
+  // One request of 32,768 tokens, 32 heads x 128: 1.10 ms, and 1.70 by the
   // other kernel; eight such requests of 8,196 tokens in all: 0.34 ms, and 0.16
   // to 0.20 by the other.
   if (few) return launch_few<DK>(a, s);
