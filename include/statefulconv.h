@@ -384,7 +384,8 @@ typedef struct {
 /* Norms of query and key heads, position rotation and cache write, for the
  * [query | key | value] rows that sc_cca_qk_conv writes. The four pages end
  * before this step: these are the usual root-mean-square norm and rotation, not
- * a form that they print. Per head x of head_dim values, all heads with one weight:
+ * a form that they print. Per head x of head_dim values, with one weight for all
+ * query heads and one for all key heads:
  *   x^ = weight * x / sqrt(mean(x^2) + eps)           (weight NULL: 1)
  *   pair i of the first rotary_dim values turns by the table's angle i:
  *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin), the pair being values
