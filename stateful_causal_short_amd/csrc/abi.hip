@@ -576,11 +576,12 @@ sc_status sc_gdn_workspace_bytes(const sc_gdn_desc* desc, int32_t batch, int64_t
   if (st != SC_OK) return st;
   if (batch < 0 || num_tokens < 0) return SC_ERR_INVALID_ARG;
   int64_t chunks = 0;
-  if ((st = gdn_chunks(desc, batch, num_tokens, &chunks)) != SC_OK) return st;
-  *bytes = batch == 0 || num_tokens == 0
-               ? 0
-               : sc::GdnWorkspace::bytes(chunks, desc->num_k_heads, desc->num_v_heads,
-                                         desc->head_k_dim, batch);
+  st = gdn_chunks(desc, batch, num_tokens, &chunks);
+  const bool empty = batch == 0 || num_tokens == 0;     // a no-op, whatever the other size
+  if (st != SC_OK && !empty) return st;
+  *bytes = empty ? 0
+                 : sc::GdnWorkspace::bytes(chunks, desc->num_k_heads, desc->num_v_heads,
+                                           desc->head_k_dim, batch);
   return SC_OK;
 }
 

@@ -43,7 +43,7 @@ constexpr int kTile = 16;        // cached tokens per tile
 constexpr int kRows = 16;        // query rows per workgroup
 constexpr int kMaxSplits = 64;
 constexpr int kSortMax = 512;    // requests put in order by their workgroups
-constexpr float kNone = -3.402823466e38f;   // running maximum before any token: no finite score is below
+constexpr float kNone = -3.402823466e38f;   // running maximum before any token, the lowest value
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 

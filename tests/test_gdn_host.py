@@ -184,3 +184,13 @@ def test_sizes_that_cannot_be_launched_are_refused_before_a_launch():
                                             ctypes.byref(n)) == UNSUPPORTED
     assert prefill(wide, batch=1 << 15, T=1) == UNSUPPORTED
     assert n.value == -7
+
+
+def test_empty_calls_need_no_workspace_whatever_their_other_size():
+    n = ctypes.c_int64(-7)
+    for batch, tokens in ((1 << 30, 0), (0, 1 << 40)):
+        assert scs.lib().sc_gdn_workspace_bytes(ctypes.byref(desc()), batch, tokens,
+                                                ctypes.byref(n)) == OK
+        assert n.value == 0
+        assert prefill(desc(), batch=batch, T=tokens, q=None, ws=None) == OK
+        n.value = -7
