@@ -469,6 +469,104 @@ sc_status sc_paged_attn_decode(const sc_paged_attn_desc* desc, const void* q, vo
                                int32_t max_seq_len, void* workspace, int64_t workspace_bytes,
                                void* stream);
 
+/* A quantised paged cache: the codes, 8-bit floats of four significant bits (e4m3, no
+ * infinities, largest 448), laid out as sc_paged_cache (strides in codes), and one
+ * scale for each token's head, 2^(byte - 127) in a byte (e8m0): (num_blocks,
+ * num_kv_heads, block_size) with a unit stride over a block's tokens. A value is its
+ * code times its scale. The library writes bytes 1 .. 247; 0 counts as 2^-127, and
+ * rows that see a token with a byte of 255 are undefined. */
+typedef struct {
+  void* data;              /* (device) */
+  int64_t block_stride, token_stride, head_stride;
+  void* scale;             /* (device) */
+  int64_t scale_block_stride, scale_head_stride;
+} sc_paged_cache_fp8;
+
+/* sc_qk_norm_rope into a quantised cache (required here). The scale of a head is the
+ * smallest power of two, from 2^-126 on, that brings its largest finite value to 448
+ * or less; values over it are rounded to the nearest code, ties to even, keys
+ * straight from fp32. Infinities and NaN become NaN codes and leave the scale to
+ * the others. Codes 4-byte aligned, strides a multiple of 4. */
+sc_status sc_qk_norm_rope_fp8(const sc_qk_norm_desc* desc, const void* q, const void* k,
+                              const void* v, void* q_out, void* k_out, const void* q_weight,
+                              const void* k_weight, const void* cos_sin, const int64_t* positions,
+                              const int64_t* slots, const sc_paged_cache_fp8* k_cache,
+                              const sc_paged_cache_fp8* v_cache, int64_t num_tokens,
+                              void* stream);
+
+typedef struct {
+  int32_t num_kv_heads;
+  int32_t head_dim;        /* 64, 128 or 256 (SC_ERR_UNSUPPORTED otherwise) */
+  int32_t block_size, num_blocks;
+  int64_t k_row_stride, v_row_stride;     /* elements, multiples of 8 */
+  int64_t block_table_row_stride;         /* >= max_blocks, >= 1 */
+} sc_cache_read_desc;
+
+/* Reads tokens of a quantised cache back as bf16 rows, exactly but for values
+ * below bf16's range: row start_loc[r] + i is token first_tokens[r] + i of request
+ * r, for start_loc[r] <= row < start_loc[r + 1]. Tokens outside the block table or in a
+ * block outside the cache read as zeros; other rows are left as they were.
+ *   k_out, v_out (device) (num_rows, num_kv_heads * head_dim) bf16, 16-byte aligned
+ *   block_table  (device) int32 (batch, max_blocks)
+ *   start_loc    (device) int32 (batch + 1), non-decreasing
+ *   first_tokens (device) int32 (batch), or NULL: every request from its first on
+ * Codes 16-byte aligned, strides a multiple of 16. */
+sc_status sc_paged_cache_read_fp8(const sc_cache_read_desc* desc, const sc_paged_cache_fp8* k_cache,
+                                  const sc_paged_cache_fp8* v_cache, void* k_out, void* v_out,
+                                  const int32_t* block_table, int32_t max_blocks,
+                                  const int32_t* start_loc, const int32_t* first_tokens,
+                                  int32_t batch, int64_t num_rows, void* stream);
+
+/* sc_paged_attn_decode over quantised caches: the same rows, visibility and
+ * arguments. Scores and weights are fp32 (weights enter the second product as two
+ * bf16 parts, 2^-16). Codes 16-byte aligned, strides a multiple of 16; scales
+ * 4-byte aligned, strides a multiple of 4. The workspace is its own function's. */
+sc_status sc_paged_attn_fp8_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
+                                            int32_t q_len, int32_t max_seq_len, int64_t* bytes);
+sc_status sc_paged_attn_decode_fp8(const sc_paged_attn_desc* desc, const void* q, void* out,
+                                   const sc_paged_cache_fp8* k_cache,
+                                   const sc_paged_cache_fp8* v_cache, const int32_t* block_table,
+                                   int32_t max_blocks, const int32_t* seq_lens, int32_t batch,
+                                   int32_t q_len, int32_t max_seq_len, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/* Attention of the newest tokens of requests that share the beginning of their
+ * caches: the rows of sc_paged_attn_decode, with each group's prefix read once for
+ * all of its requests. Requests [group_start_loc[g], group_start_loc[g + 1]) hold the
+ * same keys and values in their first prefix_lens[g] tokens, in the same blocks or
+ * copies of them: they are read where the first such request has them whose new
+ * tokens all see the whole prefix. Requests whose new tokens do not (short ones,
+ * rows that pad a captured batch) and those of no group are taken as
+ * sc_paged_attn_decode takes them, whatever the others hold.
+ *   group_start_loc (device) int32 (num_groups + 1), non-decreasing, in [0, batch]
+ *   prefix_lens     (device) int32 (num_groups), clamped to [0, max_prefix_len]; any
+ *                   length, in whole blocks or not
+ *   num_groups      (host) >= 0; with 0 both arrays may be NULL
+ *   max_prefix_len  (host) <= max_seq_len; the split of the prefixes follows from it
+ * block_table rows hold a request's whole cache, its prefix first. Over the prefix,
+ * weights are rounded to bf16 (their sum is of the rounded ones); everything else is
+ * as in sc_paged_attn_decode and sc_paged_attn_decode_fp8. Other arguments, limits
+ * and alignment are theirs; one workspace function serves both caches. */
+sc_status sc_paged_attn_prefix_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
+                                               int32_t q_len, int32_t max_seq_len,
+                                               int32_t num_groups, int32_t max_prefix_len,
+                                               int64_t* bytes);
+sc_status sc_paged_attn_prefix(const sc_paged_attn_desc* desc, const void* q, void* out,
+                               const sc_paged_cache* k_cache, const sc_paged_cache* v_cache,
+                               const int32_t* block_table, int32_t max_blocks,
+                               const int32_t* seq_lens, const int32_t* group_start_loc,
+                               const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
+                               int32_t q_len, int32_t max_seq_len, int32_t max_prefix_len,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+sc_status sc_paged_attn_prefix_fp8(const sc_paged_attn_desc* desc, const void* q, void* out,
+                                   const sc_paged_cache_fp8* k_cache,
+                                   const sc_paged_cache_fp8* v_cache, const int32_t* block_table,
+                                   int32_t max_blocks, const int32_t* seq_lens,
+                                   const int32_t* group_start_loc, const int32_t* prefix_lens,
+                                   int32_t num_groups, int32_t batch, int32_t q_len,
+                                   int32_t max_seq_len, int32_t max_prefix_len, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
 /* Checks the device-side preconditions the calls above document but cannot
  * check without a host sync (a debugging and test aid, not for the hot path):
  * waits for `stream`, copies the metadata to the host and returns

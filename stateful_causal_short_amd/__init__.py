@@ -1,6 +1,7 @@
 """MI355X (gfx950) stateful causal short convolution, and the operators that
 take its outputs: the gated delta rule (prefill, update, speculative update),
-head norms with rotation and cache write, and paged decode attention.
+head norms with rotation and cache write (bf16 or quantised), the quantised
+cache's read, paged decode attention, and attention over shared prefixes.
 
 Thin Python binding of ``libstatefulconv.so`` (C ABI in
 ``include/statefulconv.h``). Every function here only marshals arguments —
@@ -34,7 +35,9 @@ EXPORTS = ("sc_conv_prefill_varlen", "sc_conv_update", "sc_conv_update_spec",
            "sc_state_scatter", "sc_cca_qk_conv", "sc_gdn_workspace_bytes",
            "sc_gdn_prefill_varlen", "sc_gdn_update", "sc_gdn_update_spec",
            "sc_qk_norm_rope", "sc_paged_attn_workspace_bytes", "sc_paged_attn_decode",
-           "sc_status_string", "sc_abi_version")
+           "sc_qk_norm_rope_fp8", "sc_paged_cache_read_fp8", "sc_paged_attn_fp8_workspace_bytes",
+           "sc_paged_attn_decode_fp8", "sc_paged_attn_prefix_workspace_bytes",
+           "sc_paged_attn_prefix", "sc_paged_attn_prefix_fp8", "sc_status_string", "sc_abi_version")
 
 
 class ScError(RuntimeError):
@@ -109,6 +112,20 @@ class sc_paged_attn_desc(ctypes.Structure):
                 ("out_row_stride", ctypes.c_int64), ("block_table_row_stride", ctypes.c_int64)]
 
 
+class sc_paged_cache_fp8(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("block_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("scale", ctypes.c_void_p), ("scale_block_stride", ctypes.c_int64),
+                ("scale_head_stride", ctypes.c_int64)]
+
+
+class sc_cache_read_desc(ctypes.Structure):
+    _fields_ = [("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("k_row_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64),
+                ("block_table_row_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -167,6 +184,22 @@ def lib():
         L.sc_paged_attn_workspace_bytes.argtypes = [PA, I32, I32, I32, ctypes.POINTER(I64)]
         L.sc_paged_attn_decode.restype = I32
         L.sc_paged_attn_decode.argtypes = [PA, P, P, PC, PC, P, I32, P, I32, I32, I32, P, I64, P]
+        L.sc_qk_norm_rope_fp8.restype = I32
+        L.sc_qk_norm_rope_fp8.argtypes = [P, P, P, P, P, P, P, P, P, P, P, PC, PC, I64, P]
+        L.sc_paged_cache_read_fp8.restype = I32
+        L.sc_paged_cache_read_fp8.argtypes = [P, PC, PC, P, P, P, I32, P, P, I32, I64, P]
+        L.sc_paged_attn_fp8_workspace_bytes.restype = I32
+        L.sc_paged_attn_fp8_workspace_bytes.argtypes = [PA, I32, I32, I32, ctypes.POINTER(I64)]
+        L.sc_paged_attn_decode_fp8.restype = I32
+        L.sc_paged_attn_decode_fp8.argtypes = [PA, P, P, PC, PC, P, I32, P, I32, I32, I32, P, I64,
+                                               P]
+        L.sc_paged_attn_prefix_workspace_bytes.restype = I32
+        L.sc_paged_attn_prefix_workspace_bytes.argtypes = [PA, I32, I32, I32, I32, I32,
+                                                           ctypes.POINTER(I64)]
+        for name in ("sc_paged_attn_prefix", "sc_paged_attn_prefix_fp8"):
+            fn = getattr(L, name)
+            fn.restype = I32
+            fn.argtypes = [PA, P, P, PC, PC, P, I32, P, P, P, I32, I32, I32, I32, I32, P, I64, P]
         L.sc_status_string.restype = ctypes.c_char_p
         L.sc_status_string.argtypes = [I32]
         L.sc_abi_version.restype = I32
@@ -581,6 +614,8 @@ _GDN_DESC = _packer(sc_gdn_desc)
 _QK_NORM_DESC = _packer(sc_qk_norm_desc)
 _ATTN_DESC = _packer(sc_paged_attn_desc)
 _CACHE_DESC = _packer(sc_paged_cache)
+_CACHE_FP8_DESC = _packer(sc_paged_cache_fp8)
+_CACHE_READ_DESC = _packer(sc_cache_read_desc)
 
 
 def _addresses(device, *tensors):
@@ -792,6 +827,12 @@ def sc_gdn_update_spec(query, key, value, a, b, A_log, dt_bias, out, state_pool,
         raise ScError("sc_gdn_update_spec", st)
 
 
+def _given(t, name):
+    if t is None:
+        raise ValueError(f"{name}: expected a tensor")
+    return t
+
+
 def _paged(cache, name, blocks, block_size, nkv, hd, dtype):
     """Packed descriptor of a (num_blocks, block_size, nkv, hd) cache tensor."""
     if cache.shape != (blocks, block_size, nkv, hd) or cache.dtype != dtype:
@@ -804,20 +845,47 @@ def _paged(cache, name, blocks, block_size, nkv, hd, dtype):
                             st[1] if block_size > 1 else 0, st[2] if nkv > 1 else 0)
 
 
-def sc_qk_norm_rope(query, key, value, q_out, k_out, q_weight, k_weight, cos_sin, positions,
-                    slots, k_cache, v_cache, *, head_dim: int, eps: float = 1e-6,
-                    interleaved: bool = False, stream=None):
-    """Norms of the query and key heads, position rotation, and the write of keys
-    and values into a paged cache.
+def _paged_fp8(cache, scale, name, blocks, block_size, nkv, hd):
+    """Packed descriptor of a quantised cache: codes as for _paged, and the scales'
+    bytes (num_blocks, nkv, block_size)."""
+    torch = _torch()
+    if cache.shape != (blocks, block_size, nkv, hd) or cache.dtype != torch.float8_e4m3fn:
+        raise ValueError(f"{name}_cache: expected ({blocks}, {block_size}, {nkv}, {hd}) of "
+                         f"{torch.float8_e4m3fn}")
+    if scale.shape != (blocks, nkv, block_size) or \
+            scale.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+        raise ValueError(f"{name}_scale: expected ({blocks}, {nkv}, {block_size}) of "
+                         f"{torch.float8_e8m0fnu} or {torch.uint8}")
+    st, sc = cache.stride(), scale.stride()
+    if st[3] != 1:
+        raise ValueError(f"{name}_cache: expected a unit stride in head_dim")
+    if sc[2] != 1 and block_size > 1:
+        raise ValueError(f"{name}_scale: expected a unit stride over a block's tokens")
+    # the stride of a dimension of one entry is never used
+    return _CACHE_FP8_DESC.pack(
+        cache.data_ptr(), st[0] if blocks > 1 else 0, st[1] if block_size > 1 else 0,
+        st[2] if nkv > 1 else 0, scale.data_ptr(), sc[0] if blocks > 1 else 0,
+        sc[1] if nkv > 1 else 0)
 
-    query (T, nq * head_dim), key, value (T, nkv * head_dim) bf16 rows (column
-    blocks of sc_cca_qk_conv's output rows will do); q_out like query; k_out
-    like key or None; q_out = query or k_out = key work in place. q_weight,
-    k_weight: (head_dim) bf16 or None. cos_sin: (positions, rotary_dim) fp32 or
-    bf16, cos then sin, or None (no rotation). positions, slots: int64 (T); slot
-    -1 is not written. k_cache, v_cache: (num_blocks, block_size, nkv,
-    head_dim), or None for both (value and slots are then not read).
-    """
+
+def _caches(k_cache, k_scale, v_cache, v_scale, nkv, hd, dtype):
+    """Blocks, block size and packed descriptors of a pair of caches, quantised if
+    they have scales."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
+    blocks, block_size = k_cache.shape[:2]
+    if k_scale is None:
+        kc = _paged(k_cache, "k_cache", blocks, block_size, nkv, hd, dtype)
+        vc = _paged(v_cache, "v_cache", blocks, block_size, nkv, hd, dtype)
+    else:
+        kc = _paged_fp8(k_cache, k_scale, "k", blocks, block_size, nkv, hd)
+        vc = _paged_fp8(v_cache, v_scale, "v", blocks, block_size, nkv, hd)
+    return blocks, block_size, kc, vc
+
+
+def _norm_call(name, query, key, value, q_out, k_out, q_weight, k_weight, cos_sin, positions,
+               slots, k_cache, k_scale, v_cache, v_scale, head_dim, eps, interleaved, stream):
+    """Marshals a norm, rotation and cache write, into either cache."""
     torch = _torch()
     if query.dim() != 2 or key.dim() != 2:
         raise ValueError("query, key: expected 2-D tensors")
@@ -837,13 +905,10 @@ def sc_qk_norm_rope(query, key, value, q_out, k_out, q_weight, k_weight, cos_sin
     if k_cache is None:
         value = slots = None
     else:
-        if k_cache.dim() != 4:
-            raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
         if value is None or slots is None:
             raise ValueError("value, slots: expected with the caches")
-        blocks, block_size = k_cache.shape[:2]
-        kc = _paged(k_cache, "k_cache", blocks, block_size, nkv, head_dim, dtype)
-        vc = _paged(v_cache, "v_cache", blocks, block_size, nkv, head_dim, dtype)
+        blocks, block_size, kc, vc = _caches(k_cache, k_scale, v_cache, v_scale, nkv, head_dim,
+                                             dtype)
         v_rs = _row_stride(value, "value", kw, T, dtype)
         if slots.dtype != torch.int64 or slots.dim() != 1 or slots.shape[0] < T or \
                 not slots.is_contiguous():
@@ -863,18 +928,108 @@ def sc_qk_norm_rope(query, key, value, q_out, k_out, q_weight, k_weight, cos_sin
         _row_stride(key, "key", kw, T, dtype), v_rs, _row_stride(q_out, "q_out", qw, T, dtype),
         0 if k_out is None else _row_stride(k_out, "k_out", kw, T, dtype), t_rs, top)
     ptr = _addresses(_device(query), query, key, value, q_out, k_out, q_weight, k_weight, cos_sin,
-                     positions, slots, k_cache, v_cache)
-    st = lib().sc_qk_norm_rope(desc, *ptr[:10], kc, vc, T, _stream(stream, query))
+                     positions, slots, k_cache, v_cache, k_scale, v_scale)
+    st = getattr(lib(), name)(desc, *ptr[:10], kc, vc, T, _stream(stream, query))
     if st != SC_OK:
-        raise ScError("sc_qk_norm_rope", st)
+        raise ScError(name, st)
 
 
-def _attn_need(desc, batch, q, max_seq_len) -> int:
+def sc_qk_norm_rope(query, key, value, q_out, k_out, q_weight, k_weight, cos_sin, positions,
+                    slots, k_cache, v_cache, *, head_dim: int, eps: float = 1e-6,
+                    interleaved: bool = False, stream=None):
+    """Norms of the query and key heads, position rotation, and the write of keys
+    and values into a paged cache.
+
+    query (T, nq * head_dim), key, value (T, nkv * head_dim) bf16 rows (column
+    blocks of sc_cca_qk_conv's output rows will do); q_out like query; k_out
+    like key or None; q_out = query or k_out = key work in place. q_weight,
+    k_weight: (head_dim) bf16 or None. cos_sin: (positions, rotary_dim) fp32 or
+    bf16, cos then sin, or None (no rotation). positions, slots: int64 (T); slot
+    -1 is not written. k_cache, v_cache: (num_blocks, block_size, nkv,
+    head_dim), or None for both (value and slots are then not read).
+    """
+    _norm_call("sc_qk_norm_rope", query, key, value, q_out, k_out, q_weight, k_weight, cos_sin,
+               positions, slots, k_cache, None, v_cache, None, head_dim, eps, interleaved, stream)
+
+
+def sc_qk_norm_rope_fp8(query, key, value, q_out, k_out, q_weight, k_weight, cos_sin, positions,
+                        slots, k_cache, k_scale, v_cache, v_scale, *, head_dim: int,
+                        eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """sc_qk_norm_rope into a quantised cache: k_cache, v_cache (num_blocks,
+    block_size, nkv, head_dim) float8_e4m3fn, k_scale, v_scale (num_blocks, nkv,
+    block_size) float8_e8m0fnu or its bytes as uint8, a power of two for each
+    token's head. The other arguments are those of sc_qk_norm_rope.
+    """
+    _norm_call("sc_qk_norm_rope_fp8", query, key, value, q_out, k_out, q_weight, k_weight, cos_sin,
+               positions, slots, _given(k_cache, "k_cache"), _given(k_scale, "k_scale"),
+               _given(v_cache, "v_cache"), _given(v_scale, "v_scale"), head_dim, eps, interleaved,
+               stream)
+
+
+def _block_table(table, batch) -> Tuple[int, int]:
+    """Row stride and row length of a block table of at least `batch` rows."""
+    shape = table.shape
+    if len(shape) != 2 or shape[0] < batch or table.dtype != _torch().int32:
+        raise ValueError(f"block_table: expected int32 ({batch}, max_blocks)")
+    rs, cs = table.stride()
+    if shape[1] > 1 and cs != 1 and shape[0]:
+        raise ValueError("block_table: expected adjacent entries in a row")
+    return (rs if shape[0] > 1 else max(shape[1], 1)), shape[1]
+
+
+def _counts(t, name, n):
+    """A contiguous int32 tensor of at least n entries."""
+    if t.dtype != _torch().int32 or t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 tensor of {n} entries")
+
+
+def sc_paged_cache_read_fp8(k_cache, k_scale, v_cache, v_scale, k_out, v_out, block_table,
+                            start_loc, first_tokens=None, *, stream=None):
+    """Reads tokens of requests back from a quantised cache, as bf16 rows.
+
+    k_out, v_out (rows, nkv * head_dim) bf16: row start_loc[r] + i becomes token
+    first_tokens[r] + i of request r; rows of no request are left as they were.
+    start_loc int32 (B + 1); block_table int32 (B, max_blocks); first_tokens int32 (B),
+    or None: from the first token on. Caches as for sc_qk_norm_rope_fp8.
+    """
+    torch = _torch()
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
+    nkv, hd = k_cache.shape[2:]
+    if k_out.dim() != 2:
+        raise ValueError("k_out: expected a 2-D tensor")
+    if start_loc.dim() != 1 or start_loc.shape[0] < 1:
+        raise ValueError("start_loc: expected a contiguous int32 tensor of batch + 1 entries")
+    rows, batch = k_out.shape[0], start_loc.shape[0] - 1
+    _counts(start_loc, "start_loc", batch + 1)
+    t_rs, width = _block_table(block_table, batch)
+    if first_tokens is not None:
+        _counts(first_tokens, "first_tokens", batch)
+    blocks, block_size, kc, vc = _caches(k_cache, _given(k_scale, "k_scale"), v_cache,
+                                         _given(v_scale, "v_scale"), nkv, hd, None)
+    desc = _CACHE_READ_DESC.pack(
+        nkv, hd, block_size, blocks, _row_stride(k_out, "k_out", nkv * hd, rows, torch.bfloat16),
+        _row_stride(v_out, "v_out", nkv * hd, rows, torch.bfloat16), t_rs)
+    ptr = _addresses(_device(k_cache), k_out, v_out, block_table, start_loc, first_tokens, k_scale,
+                     v_cache, v_scale)
+    st = lib().sc_paged_cache_read_fp8(desc, kc, vc, ptr[0], ptr[1], ptr[2], width, ptr[3], ptr[4],
+                                       batch, rows, _stream(stream, k_cache))
+    if st != SC_OK:
+        raise ScError("sc_paged_cache_read_fp8", st)
+
+
+def _workspace_need(name, desc, *sizes) -> int:
     n = ctypes.c_int64(0)
-    st = lib().sc_paged_attn_workspace_bytes(desc, batch, q, max_seq_len, ctypes.byref(n))
+    st = getattr(lib(), name)(desc, *sizes, ctypes.byref(n))
     if st != SC_OK:
-        raise ScError("sc_paged_attn_workspace_bytes", st)
+        raise ScError(name, st)
     return n.value
+
+
+def _heads_desc(num_q_heads, num_kv_heads, head_dim):
+    """Descriptor of these heads, for the sizes of a workspace."""
+    w = num_q_heads * head_dim
+    return _ATTN_DESC.pack(num_q_heads, num_kv_heads, head_dim, SC_DTYPE_BF16, 16, 1, 1.0, w, w, 1)
 
 
 def sc_paged_attn_workspace_bytes(batch: int, *, q: int = 1, max_seq_len: int, num_q_heads: int,
@@ -882,9 +1037,68 @@ def sc_paged_attn_workspace_bytes(batch: int, *, q: int = 1, max_seq_len: int, n
     """Bytes of workspace that sc_paged_attn_decode needs for these sizes on the
     current device (0 where the cache's length is not split)."""
     _fits(32, batch=batch, q=q, max_seq_len=max_seq_len)
-    w = num_q_heads * head_dim
-    return _attn_need(_ATTN_DESC.pack(num_q_heads, num_kv_heads, head_dim, SC_DTYPE_BF16, 16, 1,
-                                      1.0, w, w, 1), batch, q, max_seq_len)
+    return _workspace_need("sc_paged_attn_workspace_bytes",
+                           _heads_desc(num_q_heads, num_kv_heads, head_dim), batch, q, max_seq_len)
+
+
+def sc_paged_attn_fp8_workspace_bytes(batch: int, *, q: int = 1, max_seq_len: int,
+                                      num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """The same for sc_paged_attn_decode_fp8."""
+    _fits(32, batch=batch, q=q, max_seq_len=max_seq_len)
+    return _workspace_need("sc_paged_attn_fp8_workspace_bytes",
+                           _heads_desc(num_q_heads, num_kv_heads, head_dim), batch, q, max_seq_len)
+
+
+def sc_paged_attn_prefix_workspace_bytes(batch: int, *, q: int = 1, max_seq_len: int,
+                                         num_groups: int, max_prefix_len: int, num_q_heads: int,
+                                         num_kv_heads: int, head_dim: int) -> int:
+    """The same for sc_paged_attn_prefix and sc_paged_attn_prefix_fp8."""
+    _fits(32, batch=batch, q=q, max_seq_len=max_seq_len, num_groups=num_groups,
+          max_prefix_len=max_prefix_len)
+    return _workspace_need("sc_paged_attn_prefix_workspace_bytes",
+                           _heads_desc(num_q_heads, num_kv_heads, head_dim), batch, q, max_seq_len,
+                           num_groups, max_prefix_len)
+
+
+def _attn_call(name, need, query, out, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens,
+               max_seq_len, q, scale, workspace, stream, groups=(), sizes=()):
+    """Marshals an attention call over either cache; `groups` and `sizes` are what one
+    with shared prefixes has besides."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
+    nkv, hd = k_cache.shape[2:]
+    if query.dim() != 2:
+        raise ValueError("query: expected a 2-D tensor")
+    rows, qw = query.shape
+    if hd < 1 or qw % hd or qw == 0:
+        raise ValueError(f"query: expected rows of heads of {hd} values")
+    if q < 1 or rows % q:
+        raise ValueError("rows must be a multiple of q >= 1")
+    if not 0 <= max_seq_len < 1 << 31:
+        raise ValueError("max_seq_len: expected 0 .. 2^31 - 1")
+    batch, dtype = rows // q, query.dtype
+    t_rs, width = _block_table(block_table, batch)
+    _counts(seq_lens, "seq_lens", batch)
+    blocks, block_size, kc, vc = _caches(k_cache, k_scale, v_cache, v_scale, nkv, hd, dtype)
+    desc = _ATTN_DESC.pack(
+        qw // hd, nkv, hd, _dtype_code(query), block_size, blocks,
+        hd ** -0.5 if scale is None else scale, _row_stride(query, "query", qw, rows, dtype),
+        _row_stride(out, "out", qw, rows, dtype), t_rs)
+    dev = _device(query)
+    raw = _stream(stream, query)
+    if workspace is None:
+        workspace = _workspace(None, _workspace_need(need, desc, batch, q, max_seq_len, *sizes),
+                               query, stream)
+    else:
+        _workspace(workspace, 0, query, stream)
+    ptr = _addresses(dev, query, out, block_table, seq_lens, workspace, *groups, k_cache, v_cache,
+                     k_scale, v_scale)
+    # (groups' arrays, their number, batch, q, max_seq_len, longest prefix)
+    more = (*ptr[5:5 + len(groups)], *sizes[:1], batch, q, max_seq_len, *sizes[1:])
+    st = getattr(lib(), name)(desc, ptr[0], ptr[1], kc, vc, ptr[2], width, ptr[3], *more, ptr[4],
+                              _nbytes(workspace), raw)
+    if st != SC_OK:
+        raise ScError(name, st)
 
 
 def sc_paged_attn_decode(query, out, k_cache, v_cache, block_table, seq_lens, *,
@@ -900,46 +1114,62 @@ def sc_paged_attn_decode(query, out, k_cache, v_cache, block_table, seq_lens, *,
     sc_paged_attn_workspace_bytes bytes to reuse (one for each call that may
     run at the same time).
     """
-    torch = _torch()
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
-    blocks, block_size, nkv, hd = k_cache.shape
-    if query.dim() != 2:
-        raise ValueError("query: expected a 2-D tensor")
-    rows, qw = query.shape
-    if hd < 1 or qw % hd or qw == 0:
-        raise ValueError(f"query: expected rows of heads of {hd} values")
-    if q < 1 or rows % q:
-        raise ValueError("rows must be a multiple of q >= 1")
-    if not 0 <= max_seq_len < 1 << 31:
-        raise ValueError("max_seq_len: expected 0 .. 2^31 - 1")
-    batch, dtype = rows // q, query.dtype
-    table = block_table.shape
-    if len(table) != 2 or table[0] < batch or block_table.dtype != torch.int32:
-        raise ValueError(f"block_table: expected int32 ({batch}, max_blocks)")
-    t_rs, t_cs = block_table.stride()
-    if table[1] > 1 and t_cs != 1 and table[0]:
-        raise ValueError("block_table: expected adjacent entries in a row")
-    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] < batch or \
-            not seq_lens.is_contiguous():
-        raise ValueError(f"seq_lens: expected a contiguous int32 tensor of {batch} entries")
-    desc = _ATTN_DESC.pack(
-        qw // hd, nkv, hd, _dtype_code(query), block_size, blocks,
-        hd ** -0.5 if scale is None else scale, _row_stride(query, "query", qw, rows, dtype),
-        _row_stride(out, "out", qw, rows, dtype), t_rs if table[0] > 1 else max(table[1], 1))
-    kc = _paged(k_cache, "k_cache", blocks, block_size, nkv, hd, dtype)
-    vc = _paged(v_cache, "v_cache", blocks, block_size, nkv, hd, dtype)
-    dev = _device(query)
-    raw = _stream(stream, query)
-    if workspace is None:
-        workspace = _workspace(None, _attn_need(desc, batch, q, max_seq_len), query, stream)
-    else:
-        _workspace(workspace, 0, query, stream)
-    ptr = _addresses(dev, query, out, block_table, seq_lens, workspace, k_cache, v_cache)
-    st = lib().sc_paged_attn_decode(desc, ptr[0], ptr[1], kc, vc, ptr[2], table[1], ptr[3], batch,
-                                    q, max_seq_len, ptr[4], _nbytes(workspace), raw)
-    if st != SC_OK:
-        raise ScError("sc_paged_attn_decode", st)
+    _attn_call("sc_paged_attn_decode", "sc_paged_attn_workspace_bytes", query, out, k_cache, None,
+               v_cache, None, block_table, seq_lens, max_seq_len, q, scale, workspace, stream)
+
+
+def sc_paged_attn_decode_fp8(query, out, k_cache, k_scale, v_cache, v_scale, block_table,
+                             seq_lens, *, max_seq_len: int, q: int = 1,
+                             scale: Optional[float] = None, workspace=None, stream=None):
+    """sc_paged_attn_decode over quantised caches (as for sc_qk_norm_rope_fp8); its
+    workspace has sc_paged_attn_fp8_workspace_bytes bytes."""
+    _attn_call("sc_paged_attn_decode_fp8", "sc_paged_attn_fp8_workspace_bytes", query, out,
+               k_cache, _given(k_scale, "k_scale"), v_cache, _given(v_scale, "v_scale"),
+               block_table, seq_lens, max_seq_len, q, scale, workspace, stream)
+
+
+def _prefix_call(name, query, out, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens,
+                 group_start_loc, prefix_lens, max_seq_len, max_prefix_len, q, scale, workspace,
+                 stream):
+    if prefix_lens.dim() != 1:
+        raise ValueError("prefix_lens: expected a 1-D tensor")
+    groups = prefix_lens.shape[0]
+    _counts(prefix_lens, "prefix_lens", groups)
+    _counts(group_start_loc, "group_start_loc", groups + 1)
+    if not 0 <= max_prefix_len < 1 << 31:
+        raise ValueError("max_prefix_len: expected 0 .. 2^31 - 1")
+    _attn_call(name, "sc_paged_attn_prefix_workspace_bytes", query, out, k_cache, k_scale, v_cache,
+               v_scale, block_table, seq_lens, max_seq_len, q, scale, workspace, stream,
+               (group_start_loc, prefix_lens), (groups, max_prefix_len))
+
+
+def sc_paged_attn_prefix(query, out, k_cache, v_cache, block_table, seq_lens, group_start_loc,
+                         prefix_lens, *, max_seq_len: int, max_prefix_len: int, q: int = 1,
+                         scale: Optional[float] = None, workspace=None, stream=None):
+    """sc_paged_attn_decode for requests that share the beginning of their caches,
+    which is read once for each group of them.
+
+    group_start_loc int32 (G + 1): group g is requests [group_start_loc[g],
+    group_start_loc[g+1]); prefix_lens int32 (G): their first tokens that are the
+    same, at most max_prefix_len. block_table rows hold whole caches, the prefix
+    first; requests too short to see the whole prefix, and those of no group, are
+    taken by themselves. workspace: None, or a tensor of
+    sc_paged_attn_prefix_workspace_bytes bytes. The other arguments are those of
+    sc_paged_attn_decode.
+    """
+    _prefix_call("sc_paged_attn_prefix", query, out, k_cache, None, v_cache, None, block_table,
+                 seq_lens, group_start_loc, prefix_lens, max_seq_len, max_prefix_len, q, scale,
+                 workspace, stream)
+
+
+def sc_paged_attn_prefix_fp8(query, out, k_cache, k_scale, v_cache, v_scale, block_table,
+                             seq_lens, group_start_loc, prefix_lens, *, max_seq_len: int,
+                             max_prefix_len: int, q: int = 1, scale: Optional[float] = None,
+                             workspace=None, stream=None):
+    """sc_paged_attn_prefix over quantised caches (as for sc_qk_norm_rope_fp8)."""
+    _prefix_call("sc_paged_attn_prefix_fp8", query, out, k_cache, _given(k_scale, "k_scale"),
+                 v_cache, _given(v_scale, "v_scale"), block_table, seq_lens, group_start_loc,
+                 prefix_lens, max_seq_len, max_prefix_len, q, scale, workspace, stream)
 
 
 __all__ = ["lib", "ScError", "LIB_PATH", "EXPORTS", "sc_conv_desc", "sc_ckpt_desc",
@@ -948,4 +1178,8 @@ __all__ = ["lib", "ScError", "LIB_PATH", "EXPORTS", "sc_conv_desc", "sc_ckpt_des
            "sc_conv_update_spec", "sc_conv_update_spec_varlen", "sc_validate_metadata",
            "sc_state_gather", "sc_state_scatter", "sc_cca_qk_conv", "sc_gdn_workspace_bytes",
            "sc_gdn_prefill_varlen", "sc_gdn_update", "sc_gdn_update_spec", "sc_qk_norm_rope",
-           "sc_paged_attn_workspace_bytes", "sc_paged_attn_decode"]
+           "sc_paged_attn_workspace_bytes", "sc_paged_attn_decode", "sc_paged_cache_fp8",
+           "sc_cache_read_desc", "sc_qk_norm_rope_fp8", "sc_paged_cache_read_fp8",
+           "sc_paged_attn_fp8_workspace_bytes", "sc_paged_attn_decode_fp8",
+           "sc_paged_attn_prefix_workspace_bytes", "sc_paged_attn_prefix",
+           "sc_paged_attn_prefix_fp8"]

@@ -3,6 +3,7 @@
 // in include/statefulconv.h.
 #include <stdint.h>
 
+#include <algorithm>
 #include <cmath>
 #include <new>
 #include <unordered_set>
@@ -202,6 +203,23 @@ sc_status check_paged(const sc_paged_cache* c, int32_t block_size, int64_t multi
   return SC_OK;
 }
 
+// A quantised cache; `multiple`: bytes that its loads and stores of codes have.
+sc_status check_paged_fp8(const sc_paged_cache_fp8* c, int32_t block_size, int64_t multiple,
+                          int64_t scale_multiple, sc::PagedCacheFp8* out) {
+  if (!c->data || !c->scale) return SC_ERR_NULL_ARG;
+  if (c->block_stride < 0 || c->token_stride < 0 || c->head_stride < 0 || block_size < 1 ||
+      c->scale_block_stride < 0 || c->scale_head_stride < 0)
+    return SC_ERR_INVALID_ARG;
+  if (c->block_stride % multiple != 0 || c->token_stride % multiple != 0 ||
+      c->head_stride % multiple != 0 || ((uintptr_t)c->data & (multiple - 1)) != 0 ||
+      c->scale_block_stride % scale_multiple != 0 || c->scale_head_stride % scale_multiple != 0 ||
+      ((uintptr_t)c->scale & (scale_multiple - 1)) != 0)
+    return SC_ERR_UNSUPPORTED;
+  *out = sc::PagedCacheFp8{c->data, c->block_stride, c->token_stride, c->head_stride,
+                           (uint8_t*)c->scale, c->scale_block_stride, c->scale_head_stride};
+  return SC_OK;
+}
+
 sc_status check_attn_desc(const sc_paged_attn_desc* d) {
   const sc_status st = check_heads(d->dtype, d->num_q_heads, d->num_kv_heads, d->head_dim);
   if (st != SC_OK) return st;
@@ -214,16 +232,8 @@ sc_status check_attn_desc(const sc_paged_attn_desc* d) {
   return SC_OK;
 }
 
-// Sizes of an attention call and its split; workspace bytes through *need.
-sc_status attn_sizes(const sc_paged_attn_desc* d, int32_t batch, int32_t q_len,
-                     int32_t max_seq_len, sc::PagedAttnArgs* a, int64_t* need) {
-  if (batch < 0 || q_len < 0 || max_seq_len < 0) return SC_ERR_INVALID_ARG;
-  // rows, row groups and the ends of splits are counted with 32 bits
-  if ((int64_t)batch * q_len * d->num_q_heads > 0x7FFFFFFFLL || max_seq_len > (1 << 30))
-    return SC_ERR_UNSUPPORTED;
-  *a = sc::PagedAttnArgs{};
-  *need = 0;
-  if (batch == 0 || q_len == 0) return SC_OK;
+void attn_fill(const sc_paged_attn_desc* d, int32_t batch, int32_t q_len, int32_t max_seq_len,
+               sc::PagedAttnArgs* a) {
   a->q_rs = d->q_row_stride;
   a->out_rs = d->out_row_stride;
   a->table_rs = d->block_table_row_stride;
@@ -236,7 +246,194 @@ sc_status attn_sizes(const sc_paged_attn_desc* d, int32_t batch, int32_t q_len,
   a->block_size = d->block_size;
   a->num_blocks = d->num_blocks;
   a->max_len = max_seq_len;
-  *need = sc::plan_paged_attn(a);
+}
+
+// Sizes of an attention call and its split; workspace bytes through *need.
+sc_status attn_sizes(const sc_paged_attn_desc* d, int32_t batch, int32_t q_len,
+                     int32_t max_seq_len, sc::PagedAttnArgs* a, int64_t* need, bool fp8 = false) {
+  if (batch < 0 || q_len < 0 || max_seq_len < 0) return SC_ERR_INVALID_ARG;
+  // rows, row groups and the ends of splits are counted with 32 bits
+  if ((int64_t)batch * q_len * d->num_q_heads > 0x7FFFFFFFLL || max_seq_len > (1 << 30))
+    return SC_ERR_UNSUPPORTED;
+  *a = sc::PagedAttnArgs{};
+  *need = 0;
+  if (batch == 0 || q_len == 0) return SC_OK;
+  attn_fill(d, batch, q_len, max_seq_len, a);
+  *need = fp8 ? sc::plan_paged_attn_fp8(a) : sc::plan_paged_attn(a);
+  return SC_OK;
+}
+
+// The same of an attention call with shared prefixes.
+sc_status prefix_sizes(const sc_paged_attn_desc* d, int32_t batch, int32_t q_len,
+                       int32_t max_seq_len, int32_t num_groups, int32_t max_prefix_len,
+                       sc::PagedAttnArgs* a, int64_t* need) {
+  if (batch < 0 || q_len < 0 || max_seq_len < 0 || num_groups < 0 || max_prefix_len < 0 ||
+      max_prefix_len > max_seq_len)
+    return SC_ERR_INVALID_ARG;
+  if ((int64_t)batch * q_len * d->num_q_heads > 0x7FFFFFFFLL || max_seq_len > (1 << 30) ||
+      num_groups > (1 << 30))
+    return SC_ERR_UNSUPPORTED;
+  *a = sc::PagedAttnArgs{};
+  *need = 0;
+  if (batch == 0 || q_len == 0) return SC_OK;
+  attn_fill(d, batch, q_len, max_seq_len, a);
+  a->groups = num_groups;
+  a->max_prefix = num_groups > 0 ? max_prefix_len : 0;
+  const int64_t bytes = sc::plan_paged_attn_prefix(a);
+  if (bytes < 0) return SC_ERR_UNSUPPORTED;
+  *need = bytes;
+  return SC_OK;
+}
+
+sc_status attn_caches(const sc_paged_cache* k, const sc_paged_cache* v, int32_t block_size,
+                      sc::PagedAttnArgs* a) {
+  const sc_status st = check_paged(k, block_size, 8, &a->kc);
+  return st != SC_OK ? st : check_paged(v, block_size, 8, &a->vc);
+}
+sc_status attn_caches(const sc_paged_cache_fp8* k, const sc_paged_cache_fp8* v, int32_t block_size,
+                      sc::PagedAttnArgs* a) {
+  const sc_status st = check_paged_fp8(k, block_size, 16, 4, &a->kc8);
+  return st != SC_OK ? st : check_paged_fp8(v, block_size, 16, 4, &a->vc8);
+}
+sc_status norm_caches(const sc_paged_cache* k, const sc_paged_cache* v, int32_t block_size,
+                      sc::QkNormArgs* a) {
+  const sc_status st = check_paged(k, block_size, 4, &a->kc);
+  return st != SC_OK ? st : check_paged(v, block_size, 4, &a->vc);
+}
+sc_status norm_caches(const sc_paged_cache_fp8* k, const sc_paged_cache_fp8* v, int32_t block_size,
+                      sc::QkNormArgs* a) {
+  const sc_status st = check_paged_fp8(k, block_size, 4, 1, &a->kc8);
+  return st != SC_OK ? st : check_paged_fp8(v, block_size, 4, 1, &a->vc8);
+}
+
+// What the attention calls have in common, from their sizes on.
+template <class Cache>
+sc_status attn_args(const sc_paged_attn_desc* d, const void* q, void* out, const Cache* k_cache,
+                    const Cache* v_cache, const int32_t* block_table, const int32_t* seq_lens,
+                    int32_t max_seq_len, void* workspace, int64_t workspace_bytes, int64_t need,
+                    sc::PagedAttnArgs* a) {
+  // no cached token anywhere: the rows are zeros, and no table is needed
+  if (!q || !out || !seq_lens || (max_seq_len > 0 && (!block_table || !k_cache || !v_cache)) ||
+      (need > 0 && !workspace))
+    return SC_ERR_NULL_ARG;
+  if (out == q || workspace_bytes < need || (need > 0 && !al16(workspace)))
+    return SC_ERR_INVALID_ARG;
+  if (max_seq_len > 0) {
+    const sc_status st = attn_caches(k_cache, v_cache, d->block_size, a);
+    if (st != SC_OK) return st;
+    if (d->num_blocks < 1) return SC_ERR_INVALID_ARG;
+  }
+  if (!al16(q) || !al8(out)) return SC_ERR_UNSUPPORTED;
+  a->q = q;
+  a->out = out;
+  a->table = block_table;
+  a->lens = seq_lens;
+  a->ws = (float*)workspace;
+  return SC_OK;
+}
+
+sc_status attn_bounds(const sc_paged_attn_desc* d, int32_t max_blocks, int32_t max_seq_len,
+                      int64_t workspace_bytes) {
+  return max_blocks < 0 || workspace_bytes < 0 || d->block_table_row_stride < max_blocks ||
+                 max_seq_len > (int64_t)max_blocks * d->block_size
+             ? SC_ERR_INVALID_ARG
+             : SC_OK;
+}
+
+template <class Cache>
+sc_status attn_prefix_call(const sc_paged_attn_desc* desc, const void* q, void* out,
+                           const Cache* k_cache, const Cache* v_cache, const int32_t* block_table,
+                           int32_t max_blocks, const int32_t* seq_lens,
+                           const int32_t* group_start_loc, const int32_t* prefix_lens,
+                           int32_t num_groups, int32_t batch, int32_t q_len, int32_t max_seq_len,
+                           int32_t max_prefix_len, void* workspace, int64_t workspace_bytes,
+                           bool fp8, void* stream) {
+  if (!desc) return SC_ERR_NULL_ARG;
+  sc_status st = check_attn_desc(desc);
+  if (st != SC_OK) return st;
+  sc::PagedAttnArgs a;
+  int64_t need = 0;
+  st = prefix_sizes(desc, batch, q_len, max_seq_len, num_groups, max_prefix_len, &a, &need);
+  if (st != SC_OK) return st;
+  if ((st = attn_bounds(desc, max_blocks, max_seq_len, workspace_bytes)) != SC_OK) return st;
+  if (batch == 0 || q_len == 0) return SC_OK;
+  if (num_groups > 0 && (!group_start_loc || !prefix_lens)) return SC_ERR_NULL_ARG;
+  st = attn_args(desc, q, out, k_cache, v_cache, block_table, seq_lens, max_seq_len, workspace,
+                 workspace_bytes, need, &a);
+  if (st != SC_OK) return st;
+  a.group_starts = group_start_loc;
+  a.prefix_lens = prefix_lens;
+  return from_hip(sc::launch_paged_attn_prefix(a, fp8, (hipStream_t)stream));
+}
+
+// Norms with either cache: the checks and arguments that both have; with no tokens
+// SC_OK and no arguments.
+template <class Cache>
+sc_status norm_args(const sc_qk_norm_desc* desc, const void* q, const void* k, const void* v,
+                    void* q_out, void* k_out, const void* q_weight, const void* k_weight,
+                    const void* cos_sin, const int64_t* positions, const int64_t* slots,
+                    const Cache* k_cache, const Cache* v_cache, int64_t num_tokens,
+                    sc::QkNormArgs* a) {
+  const int nq = desc->num_q_heads, nkv = desc->num_kv_heads, hd = desc->head_dim;
+  const sc_status st = check_heads(desc->dtype, nq, nkv, hd);
+  if (st != SC_OK) return st;
+  if (desc->table_dtype != SC_DTYPE_F32 && desc->table_dtype != SC_DTYPE_BF16)
+    return SC_ERR_DTYPE;
+  const int rot = desc->rotary_dim;
+  if (rot < 0 || rot > hd || (desc->interleaved != 0 && desc->interleaved != 1) ||
+      !(desc->eps >= 0) || num_tokens < 0 || desc->num_blocks < 0)
+    return SC_ERR_INVALID_ARG;
+  if (rot % 8 != 0) return SC_ERR_UNSUPPORTED;
+  const int64_t qw = (int64_t)nq * hd, kw = (int64_t)nkv * hd;
+  if (desc->q_row_stride < qw || desc->k_row_stride < kw || desc->q_out_row_stride < qw ||
+      (k_out && desc->k_out_row_stride < kw) || (k_cache && desc->v_row_stride < kw) ||
+      (rot > 0 && (desc->table_row_stride < rot || desc->max_position < 1)))
+    return SC_ERR_INVALID_ARG;
+  if (!k_cache != !v_cache) return SC_ERR_NULL_ARG;
+  if (num_tokens == 0) return SC_OK;
+  if (!q || !k || !q_out || (rot > 0 && (!cos_sin || !positions)) || (k_cache && (!v || !slots)))
+    return SC_ERR_NULL_ARG;
+  // in place only on the same rows: a lane then rewrites what it alone has read
+  if ((q_out == q && desc->q_out_row_stride != desc->q_row_stride) ||
+      (k_out && k_out == k && desc->k_out_row_stride != desc->k_row_stride) || q_out == k ||
+      q_out == k_out || k_out == q)
+    return SC_ERR_INVALID_ARG;
+  if (k_cache) {
+    const sc_status bad = norm_caches(k_cache, v_cache, desc->block_size, a);
+    if (bad != SC_OK) return bad;
+  }
+  if (!al8(q) || !al8(k) || !al8(q_out) || !al8(k_out) || !al8(q_weight) || !al8(k_weight) ||
+      (k_cache && (!al8(v) || desc->v_row_stride % 4 != 0)) || desc->q_row_stride % 4 != 0 ||
+      desc->k_row_stride % 4 != 0 || desc->q_out_row_stride % 4 != 0 ||
+      (k_out && desc->k_out_row_stride % 4 != 0))
+    return SC_ERR_UNSUPPORTED;
+  a->q = q;
+  a->k = k;
+  a->v = v;
+  a->q_out = q_out;
+  a->k_out = k_out;
+  a->q_w = q_weight;
+  a->k_w = k_weight;
+  a->table = cos_sin;
+  a->positions = positions;
+  a->slots = k_cache ? slots : nullptr;
+  a->q_rs = desc->q_row_stride;
+  a->k_rs = desc->k_row_stride;
+  a->v_rs = desc->v_row_stride;
+  a->qo_rs = desc->q_out_row_stride;
+  a->ko_rs = desc->k_out_row_stride;
+  a->table_rs = desc->table_row_stride;
+  a->max_pos = desc->max_position;
+  a->num_tokens = num_tokens;
+  a->eps = desc->eps;
+  a->nq = nq;
+  a->nkv = nkv;
+  a->hd = hd;
+  a->rot = rot;
+  a->interleaved = desc->interleaved;
+  a->table_f32 = desc->table_dtype == SC_DTYPE_F32;
+  a->block_size = desc->block_size;
+  a->num_blocks = desc->num_blocks;
   return SC_OK;
 }
 
@@ -667,68 +864,67 @@ sc_status sc_qk_norm_rope(const sc_qk_norm_desc* desc, const void* q, const void
                           const int64_t* slots, const sc_paged_cache* k_cache,
                           const sc_paged_cache* v_cache, int64_t num_tokens, void* stream) {
   if (!desc) return SC_ERR_NULL_ARG;
-  const int nq = desc->num_q_heads, nkv = desc->num_kv_heads, hd = desc->head_dim;
-  sc_status st = check_heads(desc->dtype, nq, nkv, hd);
-  if (st != SC_OK) return st;
-  if (desc->table_dtype != SC_DTYPE_F32 && desc->table_dtype != SC_DTYPE_BF16)
-    return SC_ERR_DTYPE;
-  const int rot = desc->rotary_dim;
-  if (rot < 0 || rot > hd || (desc->interleaved != 0 && desc->interleaved != 1) ||
-      !(desc->eps >= 0) || num_tokens < 0 || desc->num_blocks < 0)
-    return SC_ERR_INVALID_ARG;
-  if (rot % 8 != 0) return SC_ERR_UNSUPPORTED;
-  const int64_t qw = (int64_t)nq * hd, kw = (int64_t)nkv * hd;
-  if (desc->q_row_stride < qw || desc->k_row_stride < kw || desc->q_out_row_stride < qw ||
-      (k_out && desc->k_out_row_stride < kw) || (k_cache && desc->v_row_stride < kw) ||
-      (rot > 0 && (desc->table_row_stride < rot || desc->max_position < 1)))
-    return SC_ERR_INVALID_ARG;
-  if (!k_cache != !v_cache) return SC_ERR_NULL_ARG;
-  if (num_tokens == 0) return SC_OK;
-  if (!q || !k || !q_out || (rot > 0 && (!cos_sin || !positions)) || (k_cache && (!v || !slots)))
-    return SC_ERR_NULL_ARG;
-  // in place only on the same rows: a lane then rewrites what it alone has read
-  if ((q_out == q && desc->q_out_row_stride != desc->q_row_stride) ||
-      (k_out && k_out == k && desc->k_out_row_stride != desc->k_row_stride) || q_out == k ||
-      q_out == k_out || k_out == q)
-    return SC_ERR_INVALID_ARG;
   sc::QkNormArgs a{};
-  if (k_cache) {
-    if ((st = check_paged(k_cache, desc->block_size, 4, &a.kc)) != SC_OK) return st;
-    if ((st = check_paged(v_cache, desc->block_size, 4, &a.vc)) != SC_OK) return st;
-  }
-  if (!al8(q) || !al8(k) || !al8(q_out) || !al8(k_out) || !al8(q_weight) || !al8(k_weight) ||
-      (k_cache && (!al8(v) || desc->v_row_stride % 4 != 0)) || desc->q_row_stride % 4 != 0 ||
-      desc->k_row_stride % 4 != 0 || desc->q_out_row_stride % 4 != 0 ||
-      (k_out && desc->k_out_row_stride % 4 != 0))
+  const sc_status st = norm_args(desc, q, k, v, q_out, k_out, q_weight, k_weight, cos_sin, positions,
+                                 slots, k_cache, v_cache, num_tokens, &a);
+  if (st != SC_OK || num_tokens == 0) return st;
+  return from_hip(sc::launch_qk_norm(a, (hipStream_t)stream));
+}
+
+sc_status sc_qk_norm_rope_fp8(const sc_qk_norm_desc* desc, const void* q, const void* k,
+                              const void* v, void* q_out, void* k_out, const void* q_weight,
+                              const void* k_weight, const void* cos_sin, const int64_t* positions,
+                              const int64_t* slots, const sc_paged_cache_fp8* k_cache,
+                              const sc_paged_cache_fp8* v_cache, int64_t num_tokens,
+                              void* stream) {
+  if (!desc || !k_cache || !v_cache) return SC_ERR_NULL_ARG;
+  sc::QkNormArgs a{};
+  const sc_status st = norm_args(desc, q, k, v, q_out, k_out, q_weight, k_weight, cos_sin, positions,
+                                 slots, k_cache, v_cache, num_tokens, &a);
+  if (st != SC_OK || num_tokens == 0) return st;
+  return from_hip(sc::launch_qk_norm_fp8(a, (hipStream_t)stream));
+}
+
+sc_status sc_paged_cache_read_fp8(const sc_cache_read_desc* desc, const sc_paged_cache_fp8* k_cache,
+                                  const sc_paged_cache_fp8* v_cache, void* k_out, void* v_out,
+                                  const int32_t* block_table, int32_t max_blocks,
+                                  const int32_t* start_loc, const int32_t* first_tokens,
+                                  int32_t batch, int64_t num_rows, void* stream) {
+  if (!desc) return SC_ERR_NULL_ARG;
+  const int nkv = desc->num_kv_heads, hd = desc->head_dim;
+  sc_status st = check_heads(SC_DTYPE_BF16, nkv, nkv, hd);
+  if (st != SC_OK) return st;
+  const int64_t w = (int64_t)nkv * hd;
+  if (desc->block_size < 1 || desc->num_blocks < 0 || desc->k_row_stride < w ||
+      desc->v_row_stride < w || max_blocks < 0 || batch < 0 || num_rows < 0 ||
+      desc->block_table_row_stride < std::max(max_blocks, 1))
+    return SC_ERR_INVALID_ARG;
+  if (desc->k_row_stride % 8 != 0 || desc->v_row_stride % 8 != 0 || num_rows > 0x7FFFFFFFLL)
     return SC_ERR_UNSUPPORTED;
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.q_out = q_out;
+  if (batch == 0 || num_rows == 0) return SC_OK;
+  if (!k_cache || !v_cache || !k_out || !v_out || !start_loc || (!block_table && max_blocks > 0))
+    return SC_ERR_NULL_ARG;
+  if (k_out == v_out) return SC_ERR_INVALID_ARG;
+  sc::CacheReadArgs a{};
+  if ((st = check_paged_fp8(k_cache, desc->block_size, 16, 1, &a.kc)) != SC_OK) return st;
+  if ((st = check_paged_fp8(v_cache, desc->block_size, 16, 1, &a.vc)) != SC_OK) return st;
+  if (!al16(k_out) || !al16(v_out)) return SC_ERR_UNSUPPORTED;
   a.k_out = k_out;
-  a.q_w = q_weight;
-  a.k_w = k_weight;
-  a.table = cos_sin;
-  a.positions = positions;
-  a.slots = k_cache ? slots : nullptr;
-  a.q_rs = desc->q_row_stride;
+  a.v_out = v_out;
+  a.table = block_table;
+  a.starts = start_loc;
+  a.first = first_tokens;
   a.k_rs = desc->k_row_stride;
   a.v_rs = desc->v_row_stride;
-  a.qo_rs = desc->q_out_row_stride;
-  a.ko_rs = desc->k_out_row_stride;
-  a.table_rs = desc->table_row_stride;
-  a.max_pos = desc->max_position;
-  a.num_tokens = num_tokens;
-  a.eps = desc->eps;
-  a.nq = nq;
+  a.table_rs = desc->block_table_row_stride;
+  a.num_rows = num_rows;
+  a.batch = batch;
   a.nkv = nkv;
   a.hd = hd;
-  a.rot = rot;
-  a.interleaved = desc->interleaved;
-  a.table_f32 = desc->table_dtype == SC_DTYPE_F32;
   a.block_size = desc->block_size;
   a.num_blocks = desc->num_blocks;
-  return from_hip(sc::launch_qk_norm(a, (hipStream_t)stream));
+  a.max_blocks = max_blocks;
+  return from_hip(sc::launch_cache_read_fp8(a, (hipStream_t)stream));
 }
 
 sc_status sc_paged_attn_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
@@ -738,6 +934,15 @@ sc_status sc_paged_attn_workspace_bytes(const sc_paged_attn_desc* desc, int32_t 
   if (st != SC_OK) return st;
   sc::PagedAttnArgs a;
   return attn_sizes(desc, batch, q_len, max_seq_len, &a, bytes);
+}
+
+sc_status sc_paged_attn_fp8_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
+                                            int32_t q_len, int32_t max_seq_len, int64_t* bytes) {
+  if (!desc || !bytes) return SC_ERR_NULL_ARG;
+  const sc_status st = check_attn_desc(desc);
+  if (st != SC_OK) return st;
+  sc::PagedAttnArgs a;
+  return attn_sizes(desc, batch, q_len, max_seq_len, &a, bytes, true);
 }
 
 sc_status sc_paged_attn_decode(const sc_paged_attn_desc* desc, const void* q, void* out,
@@ -752,28 +957,68 @@ sc_status sc_paged_attn_decode(const sc_paged_attn_desc* desc, const void* q, vo
   sc::PagedAttnArgs a;
   int64_t need = 0;
   if ((st = attn_sizes(desc, batch, q_len, max_seq_len, &a, &need)) != SC_OK) return st;
-  if (max_blocks < 0 || workspace_bytes < 0 || desc->block_table_row_stride < max_blocks ||
-      max_seq_len > (int64_t)max_blocks * desc->block_size)
-    return SC_ERR_INVALID_ARG;
+  if ((st = attn_bounds(desc, max_blocks, max_seq_len, workspace_bytes)) != SC_OK) return st;
   if (batch == 0 || q_len == 0) return SC_OK;
-  // no cached token anywhere: the rows are zeros, and no table is needed
-  if (!q || !out || !seq_lens || (max_seq_len > 0 && (!block_table || !k_cache || !v_cache)) ||
-      (need > 0 && !workspace))
-    return SC_ERR_NULL_ARG;
-  if (out == q || workspace_bytes < need || (need > 0 && !al16(workspace)))
-    return SC_ERR_INVALID_ARG;
-  if (max_seq_len > 0) {
-    if ((st = check_paged(k_cache, desc->block_size, 8, &a.kc)) != SC_OK) return st;
-    if ((st = check_paged(v_cache, desc->block_size, 8, &a.vc)) != SC_OK) return st;
-    if (desc->num_blocks < 1) return SC_ERR_INVALID_ARG;
-  }
-  if (!al16(q) || !al8(out)) return SC_ERR_UNSUPPORTED;
-  a.q = q;
-  a.out = out;
-  a.table = block_table;
-  a.lens = seq_lens;
-  a.ws = (float*)workspace;
+  st = attn_args(desc, q, out, k_cache, v_cache, block_table, seq_lens, max_seq_len, workspace,
+                 workspace_bytes, need, &a);
+  if (st != SC_OK) return st;
   return from_hip(sc::launch_paged_attn(a, (hipStream_t)stream));
+}
+
+sc_status sc_paged_attn_decode_fp8(const sc_paged_attn_desc* desc, const void* q, void* out,
+                                   const sc_paged_cache_fp8* k_cache,
+                                   const sc_paged_cache_fp8* v_cache, const int32_t* block_table,
+                                   int32_t max_blocks, const int32_t* seq_lens, int32_t batch,
+                                   int32_t q_len, int32_t max_seq_len, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+  if (!desc) return SC_ERR_NULL_ARG;
+  sc_status st = check_attn_desc(desc);
+  if (st != SC_OK) return st;
+  sc::PagedAttnArgs a;
+  int64_t need = 0;
+  if ((st = attn_sizes(desc, batch, q_len, max_seq_len, &a, &need, true)) != SC_OK) return st;
+  if ((st = attn_bounds(desc, max_blocks, max_seq_len, workspace_bytes)) != SC_OK) return st;
+  if (batch == 0 || q_len == 0) return SC_OK;
+  st = attn_args(desc, q, out, k_cache, v_cache, block_table, seq_lens, max_seq_len, workspace,
+                 workspace_bytes, need, &a);
+  if (st != SC_OK) return st;
+  return from_hip(sc::launch_paged_attn_fp8(a, (hipStream_t)stream));
+}
+
+sc_status sc_paged_attn_prefix_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
+                                               int32_t q_len, int32_t max_seq_len,
+                                               int32_t num_groups, int32_t max_prefix_len,
+                                               int64_t* bytes) {
+  if (!desc || !bytes) return SC_ERR_NULL_ARG;
+  const sc_status st = check_attn_desc(desc);
+  if (st != SC_OK) return st;
+  sc::PagedAttnArgs a;
+  return prefix_sizes(desc, batch, q_len, max_seq_len, num_groups, max_prefix_len, &a, bytes);
+}
+
+sc_status sc_paged_attn_prefix(const sc_paged_attn_desc* desc, const void* q, void* out,
+                               const sc_paged_cache* k_cache, const sc_paged_cache* v_cache,
+                               const int32_t* block_table, int32_t max_blocks,
+                               const int32_t* seq_lens, const int32_t* group_start_loc,
+                               const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
+                               int32_t q_len, int32_t max_seq_len, int32_t max_prefix_len,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+  return attn_prefix_call(desc, q, out, k_cache, v_cache, block_table, max_blocks, seq_lens,
+                          group_start_loc, prefix_lens, num_groups, batch, q_len, max_seq_len,
+                          max_prefix_len, workspace, workspace_bytes, false, stream);
+}
+
+sc_status sc_paged_attn_prefix_fp8(const sc_paged_attn_desc* desc, const void* q, void* out,
+                                   const sc_paged_cache_fp8* k_cache,
+                                   const sc_paged_cache_fp8* v_cache, const int32_t* block_table,
+                                   int32_t max_blocks, const int32_t* seq_lens,
+                                   const int32_t* group_start_loc, const int32_t* prefix_lens,
+                                   int32_t num_groups, int32_t batch, int32_t q_len,
+                                   int32_t max_seq_len, int32_t max_prefix_len, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+  return attn_prefix_call(desc, q, out, k_cache, v_cache, block_table, max_blocks, seq_lens,
+                          group_start_loc, prefix_lens, num_groups, batch, q_len, max_seq_len,
+                          max_prefix_len, workspace, workspace_bytes, true, stream);
 }
 
 }  // extern "C"

@@ -27,25 +27,13 @@
 // over up to 8,192 tokens 116-135 + 9 us, where uneven splits and the start and
 // end of each workgroup show; one request of 300 tokens 10.8 us: a wave's five
 // tiles in turn, each page -> key -> softmax -> values, on four CUs, and the join.
-#include "attn.hpp"
-#include "common.hpp"
+#include "attn_device.hpp"
 
 #include <algorithm>
 
 namespace sc {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
 namespace {
-
-constexpr int kTile = 16;        // cached tokens per tile
-constexpr int kRows = 16;        // query rows per workgroup
-constexpr int kMaxSplits = 64;
-constexpr int kSortMax = 512;    // requests put in order by their workgroups
-constexpr float kNone = -3.402823466e38f;   // running maximum before any token, the lowest value
-
-__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Two bf16 values, infinities and NaN replaced by zero.
 __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
@@ -57,49 +45,12 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
 template <int N>
 using ValueRun = uint32_t __attribute__((ext_vector_type(N / 2)));
 
-// The i-th request in order of falling length, in 64 steps of max_len and by
-// index within a step; a batch of up to kSortMax, its lengths spread over the
-// lanes. The step of the i-th is found bit by bit, then its place in the step.
-__device__ __forceinline__ int by_length(const PagedAttnArgs& a, int i) {
-  const int lane = (int)(threadIdx.x & 63);
-  const int drop = max(26 - __builtin_clz(a.max_len | 1), 0);   // 6 bits are left
-  int key[kSortMax / 64];
-#pragma unroll
-  for (int u = 0; u < kSortMax / 64; ++u) {
-    const int r = u * 64 + lane;
-    key[u] = r < a.batch ? min(max(a.lens[r], 0), a.max_len) >> drop : -1;
-  }
-  int step = 0;                     // the highest with more than i requests at or above it
-#pragma unroll
-  for (int bit = 32; bit > 0; bit >>= 1) {
-    int n = 0;
-#pragma unroll
-    for (int u = 0; u < kSortMax / 64; ++u) n += __popcll(__ballot(key[u] >= (step | bit)));
-    if (n > i) step |= bit;
-  }
-  int at = 0;
-#pragma unroll
-  for (int u = 0; u < kSortMax / 64; ++u) i -= __popcll(__ballot(key[u] > step));
-#pragma unroll
-  for (int u = 0; u < kSortMax / 64; ++u) {
-    const uint64_t in = __ballot(key[u] == step);
-    const int n = __popcll(in);
-    if (i >= 0 && i < n) {
-      const int below = __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
-      at = u * 64 + __ffsll(__ballot(key[u] == step && below == i)) - 1;
-    }
-    i -= n;
-  }
-  return at;
-}
-
-// Workspace: the maximum and the sum of each (query row, split), then, 16-byte
-// aligned, its hd values. The float at which those begin, for n of them:
-__host__ __device__ inline int64_t values_at(int64_t n) { return (n * 2 + 3) & ~(int64_t)3; }
-
 }  // namespace
 
-template <int HD>
+// AFTER: the call's second half behind attn_prefix. A request's tiles begin where
+// its shared tokens end (inside a tile or not), its splits are equal parts of what
+// is left, and the parts go behind the prefix's in the workspace.
+template <int HD, bool AFTER>
 __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAttnArgs a) {
   constexpr int KS = HD / 32;               // score products per tile
   constexpr int VPL = HD / 16;              // values of a token's row per lane
@@ -117,12 +68,18 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
   id /= (unsigned)a.batch;
   const int rg = (int)(id % (unsigned)row_groups);
   const int split = (int)(id / (unsigned)row_groups);
-  if (a.sorted) r = by_length(a, r);
+  if (!AFTER && a.sorted) r = by_length(a, r);
 
   const int lane = (int)(threadIdx.x & 63);
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l16 = lane & 15, lg = lane >> 4;
-  const int t_lo = split * a.split_len;
+  int start = 0, split_len = a.split_len;
+  if constexpr (AFTER) {
+    const int len = min(max(a.lens[r], 0), a.max_len);
+    start = shared_tokens(a, r, len);
+    split_len = own_split_len(a, start, len, 4 * kTile);
+  }
+  const int t_lo = (start & ~(kTile - 1)) + split * split_len;
   // Page ids run two tiles ahead of their use: a load that waits for another
   // load waits for the memory queue twice. They do not wait for the length
   // either: a tile below max_len has an entry in the table.
@@ -131,7 +88,7 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
   int t0 = t_lo + w * kTile;
   int page = page_of(t0), page_next = page_of(t0 + 4 * kTile);
   const int len = min(max(a.lens[r], 0), a.max_len);
-  const int t_hi = min(len, t_lo + a.split_len);
+  const int t_hi = min(len, t_lo + split_len);
   if (split > 0 && t_lo >= len) return;      // the join does not read such a split
 
   // this lane's query row: head kvh * group + g of new token j
@@ -205,7 +162,7 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + lg * 4 + i;
       // positions behind the tile's last visible one hold anything, NaN included
-      s[i] = cur.ok && t <= limit && t < t_hi ? s[i] * c : -INFINITY;
+      s[i] = cur.ok && t <= limit && t < t_hi && (!AFTER || t >= start) ? s[i] * c : -INFINITY;
       top = fmaxf(top, s[i]);
     }
     top = fmaxf(top, __shfl_xor(top, 16));
@@ -248,7 +205,8 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool live = cur.ok && t0 + lg * 4 + i < t_hi;
+      const int t = t0 + lg * 4 + i;
+      const bool live = cur.ok && t < t_hi && (!AFTER || t >= start);
 #pragma unroll
       for (int u = 0; u < VW; ++u) {
 #pragma unroll
@@ -317,11 +275,14 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
     fx[x] = exp2_(ml[x][l16] - mt);
     lt += ll[x][l16] * fx[x];
   }
-  const float inv = a.splits > 1 ? 1.f : (lt > 0.f ? 1.f / lt : 0.f);
+  const bool parts = AFTER || a.splits > 1;
+  const float inv = parts ? 1.f : (lt > 0.f ? 1.f / lt : 0.f);
   const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
-  float* const wo = a.ws + values_at(n_rows * a.splits);
-  const int64_t part = (q_row * a.nq + head) * a.splits + split;
-  if (a.splits > 1 && row_ok && lg == 0) {
+  const int row_parts = AFTER ? a.prefix_splits + a.splits : a.splits;
+  const int my_part = AFTER ? a.prefix_splits + split : split;
+  float* const wo = a.ws + values_at(n_rows * row_parts);
+  const int64_t part = (q_row * a.nq + head) * row_parts + my_part;
+  if (parts && row_ok && lg == 0) {
     a.ws[part * 2] = mt;
     a.ws[part * 2 + 1] = lt;
   }
@@ -343,8 +304,8 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
       for (int e = 0; e < 4; ++e)
         y[e] = (O[u * 4 + e][i] * g0 + a1[e] * g1 + a2[e] * g2 + a3[e] * g3) * gi;
       if (rr < rows) {
-        if (a.splits > 1) {
-          *(f32x4*)(wo + ((qr * a.nq + hh) * a.splits + split) * HD + col) = y;
+        if (parts) {
+          *(f32x4*)(wo + ((qr * a.nq + hh) * row_parts + my_part) * HD + col) = y;
         } else {
           f32x2 y0 = {y[0], y[1]}, y1 = {y[2], y[3]};
           *(uint2*)((uint16_t*)a.out + qr * a.out_rs + (int64_t)hh * HD + col) =
@@ -439,20 +400,41 @@ int64_t plan_paged_attn(PagedAttnArgs* a) {
   return (values_at(parts) + parts * a->hd) * (int64_t)sizeof(float);
 }
 
+int64_t own_attn_grid(const PagedAttnArgs& a) {
+  const int64_t rows = (int64_t)(a.nq / a.nkv) * a.nq_tok;
+  return (int64_t)a.batch * a.nkv * ((rows + kRows - 1) / kRows) * a.splits;
+}
+
+// Requests' own tokens behind their shared prefix, into the workspace.
+hipError_t launch_paged_attn_after(const PagedAttnArgs& a, hipStream_t s) {
+  const int64_t grid = own_attn_grid(a);
+  if (grid > 0x7FFFFFFFLL) return hipErrorNotSupported;
+  const dim3 g((unsigned)grid), b(kBlock);
+  if (a.hd == 64) hipLaunchKernelGGL((attn_split<64, true>), g, b, 0, s, a);
+  else if (a.hd == 128) hipLaunchKernelGGL((attn_split<128, true>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((attn_split<256, true>), g, b, 0, s, a);
+  return hipGetLastError();
+}
+
 namespace {
 template <int HD>
 hipError_t launch_hd(const PagedAttnArgs& a, hipStream_t s) {
-  const int64_t rows = (int64_t)(a.nq / a.nkv) * a.nq_tok;
-  const int64_t grid = (int64_t)a.batch * a.nkv * ((rows + kRows - 1) / kRows) * a.splits;
+  const int64_t grid = own_attn_grid(a);
   if (grid > 0x7FFFFFFFLL) return hipErrorNotSupported;
-  hipLaunchKernelGGL((attn_split<HD>), dim3((unsigned)grid), dim3(kBlock), 0, s, a);
+  hipLaunchKernelGGL((attn_split<HD, false>), dim3((unsigned)grid), dim3(kBlock), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
-  hipLaunchKernelGGL((attn_join<HD>), dim3((unsigned)n_rows), dim3(kBlock), 0, s, a);
-  return hipGetLastError();
+  return launch_attn_join(a, s);
 }
 }  // namespace
+
+hipError_t launch_attn_join(const PagedAttnArgs& a, hipStream_t s) {
+  const dim3 rows((unsigned)((int64_t)a.batch * a.nq_tok * a.nq)), b(kBlock);
+  if (a.hd == 64) hipLaunchKernelGGL((attn_join<64>), rows, b, 0, s, a);
+  else if (a.hd == 128) hipLaunchKernelGGL((attn_join<128>), rows, b, 0, s, a);
+  else hipLaunchKernelGGL((attn_join<256>), rows, b, 0, s, a);
+  return hipGetLastError();
+}
 
 hipError_t launch_paged_attn(const PagedAttnArgs& a, hipStream_t s) {
   switch (a.hd) {

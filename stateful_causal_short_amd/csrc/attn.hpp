@@ -1,5 +1,5 @@
-// Argument blocks and launchers of the head norms with rotation and of the
-// paged decode attention, shared by qk_norm.hip, attn.hip and abi.hip.
+// Argument blocks and launchers of the head norms with rotation, of the quantised
+// cache's read and of attention over paged caches, shared by their kernels and abi.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -14,6 +14,15 @@ struct PagedCache {
   int64_t block_s, token_s, head_s;
 };
 
+// A quantised cache: e4m3 codes laid out as above, and a scale 2^(byte - 127) for each
+// (block, head, token), tokens adjacent, at strides of the first two.
+struct PagedCacheFp8 {
+  void* p;
+  int64_t block_s, token_s, head_s;
+  uint8_t* scale;
+  int64_t scale_block_s, scale_head_s;
+};
+
 struct QkNormArgs {
   const void* q;
   const void* k;
@@ -26,6 +35,7 @@ struct QkNormArgs {
   const int64_t* positions;
   const int64_t* slots;      // nullable without caches
   PagedCache kc, vc;         // p nullable: no write
+  PagedCacheFp8 kc8, vc8;    // quantised caches in their place
   int64_t q_rs, k_rs, v_rs, qo_rs, ko_rs, table_rs, max_pos;
   int64_t num_tokens;
   float eps;
@@ -36,19 +46,47 @@ struct PagedAttnArgs {
   const void* q;
   void* out;
   PagedCache kc, vc;
+  PagedCacheFp8 kc8, vc8;    // quantised caches in their place
   const int32_t* table;      // (batch, max_blocks) at table_rs
   const int32_t* lens;
   float* ws;                 // partial results when split, else nullptr
   int64_t q_rs, out_rs, table_rs;
   float scale;
   int32_t batch, nq_tok, nq, nkv, hd, block_size, num_blocks, max_len;
-  int32_t splits, split_len, sorted; // set by plan_paged_attn
+  int32_t splits, split_len, sorted; // set by the plans
+  // requests [group_starts[g], group_starts[g + 1]) share prefix_lens[g] leading tokens
+  const int32_t* group_starts;
+  const int32_t* prefix_lens;
+  int32_t groups, max_prefix;
+  int32_t prefix_splits, prefix_split_len, waves, row_tiles;   // set by plan_paged_attn_prefix
+};
+
+struct CacheReadArgs {
+  PagedCacheFp8 kc, vc;
+  void* k_out;
+  void* v_out;
+  const int32_t* table;      // (batch, max_blocks) at table_rs
+  const int32_t* starts;     // (batch + 1): rows of each request
+  const int32_t* first;      // nullable: first token of each request
+  int64_t k_rs, v_rs, table_rs, num_rows;
+  int32_t batch, nkv, hd, block_size, num_blocks, max_blocks;
 };
 
 // Splits of the cache's length and the workspace they need (bytes).
 int64_t plan_paged_attn(PagedAttnArgs* a);
+int64_t plan_paged_attn_fp8(PagedAttnArgs* a);
+int64_t plan_paged_attn_prefix(PagedAttnArgs* a);   // -1: more workgroups than a launch has
+// Workgroups of the requests' own tokens.
+int64_t own_attn_grid(const PagedAttnArgs& a);
 
 hipError_t launch_qk_norm(const QkNormArgs& a, hipStream_t stream);
+hipError_t launch_qk_norm_fp8(const QkNormArgs& a, hipStream_t stream);
+hipError_t launch_cache_read_fp8(const CacheReadArgs& a, hipStream_t stream);
 hipError_t launch_paged_attn(const PagedAttnArgs& a, hipStream_t stream);
+hipError_t launch_paged_attn_fp8(const PagedAttnArgs& a, hipStream_t stream);
+hipError_t launch_paged_attn_after(const PagedAttnArgs& a, hipStream_t stream);
+hipError_t launch_paged_attn_after_fp8(const PagedAttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_join(const PagedAttnArgs& a, hipStream_t stream);
+hipError_t launch_paged_attn_prefix(const PagedAttnArgs& a, bool fp8, hipStream_t stream);
 
 }  // namespace sc

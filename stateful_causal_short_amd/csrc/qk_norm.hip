@@ -16,6 +16,7 @@
 // latency of three dependent loads.
 #include "attn.hpp"
 #include "common.hpp"
+#include "fp8_device.hpp"
 
 #include <algorithm>
 
@@ -43,14 +44,41 @@ __device__ __forceinline__ float head_sum(float x) {
   return x;
 }
 
+// Largest finite magnitude of a head (its bits), over its lanes.
+template <int L>
+__device__ __forceinline__ uint32_t head_top(const float* x) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t u = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+    top = max(top, u < 0x7F800000u ? u : 0u);
+  }
+#pragma unroll
+  for (int d = L / 2; d >= 1; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+  return top;
+}
+
+// A lane's two runs of four values of a head, quantised to their cache row: keys
+// straight from fp32, one rounding. `row` is the head's place, d0 and d1 the runs'.
+template <int L>
+__device__ __forceinline__ void store_fp8(const float* x, const PagedCacheFp8& c, int64_t block,
+                                          int64_t in_block, int h, int d0, int d1, bool first) {
+  const int byte = scale_byte(head_top<L>(x));
+  const float inv = scale_inverse(byte);
+  uint8_t* p = (uint8_t*)c.p + block * c.block_s + in_block * c.token_s + h * c.head_s;
+  *(uint32_t*)(p + d0) = to_fp8(x, inv);
+  *(uint32_t*)(p + d1) = to_fp8(x + 4, inv);
+  if (first) c.scale[block * c.scale_block_s + h * c.scale_head_s + in_block] = (uint8_t)byte;
+}
+
 }  // namespace
 
 // Token blockIdx.x * PER + ..., heads [per blockIdx.y, per (blockIdx.y + 1)) of
 // its query, key and (copied to the cache) value heads.
-template <int HD, int N>
+template <int HD, int N, bool FP8>
 __global__ __launch_bounds__(kBlock) void qk_norm_rope(QkNormArgs a, int per) {
   constexpr int L = HD / 8, PER = kBlock / L;
-  const int heads = a.nq + a.nkv + (a.vc.p ? a.nkv : 0);
+  const int heads = a.nq + a.nkv + (FP8 || a.vc.p ? a.nkv : 0);
   const int64_t t = (int64_t)blockIdx.x * PER + threadIdx.x / L;
   const int l = (int)(threadIdx.x % L);
   if (t >= a.num_tokens) return;               // whole heads leave: sums stay within a head
@@ -115,6 +143,13 @@ __global__ __launch_bounds__(kBlock) void qk_norm_rope(QkNormArgs a, int per) {
       if (h >= h_hi) break;
       if (h >= a.nq + a.nkv) {                 // a value head: copied
         if (block >= 0) {
+          if constexpr (FP8) {
+            float x[8];
+            unpack4(x0[n], x);
+            unpack4(x1[n], x + 4);
+            store_fp8<L>(x, a.vc8, block, in_block, h - a.nq - a.nkv, l * 8, l * 8 + 4, l == 0);
+            continue;
+          }
           uint16_t* d = vc + (int64_t)(h - a.nq - a.nkv) * a.vc.head_s + l * 8;
           *(uint2*)d = x0[n];
           *(uint2*)(d + 4) = x1[n];
@@ -162,6 +197,10 @@ __global__ __launch_bounds__(kBlock) void qk_norm_rope(QkNormArgs a, int per) {
         *(uint2*)(d + d1) = y1;
       }
       if (!is_q && block >= 0) {
+        if constexpr (FP8) {
+          store_fp8<L>(x, a.kc8, block, in_block, h - a.nq, d0, d1, l == 0);
+          continue;
+        }
         uint16_t* d = kc + (int64_t)(h - a.nq) * a.kc.head_s;
         *(uint2*)(d + d0) = y0;
         *(uint2*)(d + d1) = y1;
@@ -171,9 +210,9 @@ __global__ __launch_bounds__(kBlock) void qk_norm_rope(QkNormArgs a, int per) {
 }
 
 namespace {
-template <int HD>
+template <int HD, bool FP8>
 hipError_t launch_hd(const QkNormArgs& a, hipStream_t s) {
-  const int64_t heads = a.nq + a.nkv + (a.vc.p ? a.nkv : 0);
+  const int64_t heads = a.nq + a.nkv + (FP8 || a.vc.p ? a.nkv : 0);
   constexpr int PER = kBlock / (HD / 8);
   const int64_t blocks = (a.num_tokens + PER - 1) / PER;
   // one head to a workgroup's lanes, and more as the tokens alone fill the chip
@@ -184,18 +223,27 @@ hipError_t launch_hd(const QkNormArgs& a, hipStream_t s) {
   if (blocks > 0x7FFFFFFFLL || ny > 65535) return hipErrorNotSupported;
   const dim3 grid((unsigned)blocks, (unsigned)ny);
   if (per >= 4)
-    hipLaunchKernelGGL((qk_norm_rope<HD, 4>), grid, dim3(kBlock), 0, s, a, (int)per);
+    hipLaunchKernelGGL((qk_norm_rope<HD, 4, FP8>), grid, dim3(kBlock), 0, s, a, (int)per);
   else
-    hipLaunchKernelGGL((qk_norm_rope<HD, 1>), grid, dim3(kBlock), 0, s, a, (int)per);
+    hipLaunchKernelGGL((qk_norm_rope<HD, 1, FP8>), grid, dim3(kBlock), 0, s, a, (int)per);
   return hipGetLastError();
 }
 }  // namespace
 
 hipError_t launch_qk_norm(const QkNormArgs& a, hipStream_t s) {
   switch (a.hd) {
-    case 64: return launch_hd<64>(a, s);
-    case 128: return launch_hd<128>(a, s);
-    case 256: return launch_hd<256>(a, s);
+    case 64: return launch_hd<64, false>(a, s);
+    case 128: return launch_hd<128, false>(a, s);
+    case 256: return launch_hd<256, false>(a, s);
+  }
+  return hipErrorNotSupported;
+}
+
+hipError_t launch_qk_norm_fp8(const QkNormArgs& a, hipStream_t s) {
+  switch (a.hd) {
+    case 64: return launch_hd<64, true>(a, s);
+    case 128: return launch_hd<128, true>(a, s);
+    case 256: return launch_hd<256, true>(a, s);
   }
   return hipErrorNotSupported;
 }
