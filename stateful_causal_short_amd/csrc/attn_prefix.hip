@@ -13,19 +13,26 @@
 // bound it from about 200 rows on and bytes below.
 //
 // A wave owns 32 rows; up to eight waves of a workgroup share tiles of 32 or 64 keys and
-// values in LDS, double buffered, on their way through registers (quantised
-// caches are widened there). Scores are taken transposed, keys as the left operand
-// of 32x32x16 bf16 products: a lane then has 16 scores of one row per 32 tokens,
-// its maximum and sum need one exchange with the other half-wave, and rescaling the
-// output is a product by a lane's own factor. The same registers, rounded to bf16,
+// values in LDS, double buffered; bf16 tiles are copied there directly, quantised ones
+// pass through registers and are widened. Scores are taken transposed, keys as the
+// left operand of 32x32x16 bf16 products: a lane then has 16 scores of one row per 32
+// tokens, its maximum and sum need one exchange with the other half-wave, and rescaling
+// the output is a product by a lane's own factor. The same registers, rounded to bf16,
 // are the right operand of the second product, values transposed x weights, whose
 // inner index counts the tokens in the order in which they lie there; the transposing
 // LDS read brings the values' columns in that order.
 //
-// Weights are rounded to bf16 (by 2^-8 of each at most), and the sum is taken of the rounded ones, so
-// that their mean stays one of the values: the error is that of the values' spread,
-// averaged over the tokens, beside 2^-8 for the output's own rounding. Scores,
-// maxima, sums and outputs are fp32.
+// Matrix instructions and exponentials take about the same time: scores run a tile
+// ahead, and both products' instructions are issued with the exponentials, LDS reads and
+// sums between them. 2,048 rows x 4 key/value heads x 128 on 32,768 tokens: 147 us, 932
+// TFLOP/s (a large bf16 library product reaches 1,158 here); with the compiler's order
+// 187, with this order and tiles through registers 174, with copies that stop the
+// counters of LDS reads 153. 7 us of it are the parts' way to the workspace.
+//
+// Weights are rounded to bf16 (by 2^-8 of each at most), and the sum is taken of the
+// rounded ones, so that their mean stays one of the values: the error is that of the
+// values' spread, averaged over the tokens, beside 2^-8 for the output's own rounding.
+// Scores, maxima, sums and outputs are fp32.
 #include "attn_device.hpp"
 #include "fp8_device.hpp"
 
@@ -48,17 +55,28 @@ constexpr float kSlack = 8.f;
 // Tokens of a tile.
 constexpr int tile_tokens(int hd, int waves) { return hd == 64 || (hd == 128 && waves >= 4) ? 64 : 32; }
 
-// Where 16-byte chunk c of a tile's row lies in it: chunks are dealt so that eight rows'
-// same chunk (a key read) and four rows' same pair of chunks (a transposing read)
-// fall into different banks.
+// Where 16-byte chunk c of a tile's row lies in it. Sixteen rows' same chunk, as the lanes
+// of a key read take them together, lie in different banks; so do four rows' same four
+// chunks, which 32 lanes of a transposing read take.
 template <int HD>
-__device__ __forceinline__ int chunk_at(int row, int c) {
-  return c ^ (HD == 64 ? (row >> 1 & 3) * 2 : (row & 7) * 2);
+__device__ __forceinline__ int key_chunk(int row, int c) {
+  return c ^ (HD == 64 ? row >> 1 & 7 : row & 15);
+}
+template <int HD>
+__device__ __forceinline__ int value_chunk(int row, int c) {
+  return c ^ (HD == 64 ? (row >> 1 & 1) * 4 : (row & 3) * 4);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   f32x2 p = {x, y};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+}
+
+// 16 bytes a lane from `bytes` behind `from` (uniform) to LDS, lane after lane. As a buffer
+// access: the counters of LDS reads go on beside it, which a global one stops.
+__device__ __forceinline__ void copy_to_lds(uint16_t* from, int bytes, uint16_t* to) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(from, (short)0, 0x7FFFFFFF, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, bytes, 0, 0, 0);
 }
 
 // The group of a row tile and the tile's number in it (-1: there is no such tile).
@@ -100,14 +118,14 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
   constexpr int CH = TN * RC / NT;            // ... of a tile, per thread
   constexpr int KS = HD / 16, DB = HD / 32, TB = TN / 32;
   static_assert(TN * RC % NT == 0 && 64 % RC == 0, "a thread's chunks, a wave's rows");
-  __shared__ __align__(16) uint16_t Kl[2][TN * HD], Vl[2][TN * HD];
-  __shared__ int live_s[2][TN / kTile];
+  // four arrays: loads into one and reads of another have no order between them
+  __shared__ __align__(16) uint16_t K0[TN * HD], K1[TN * HD], V0[TN * HD], V1[TN * HD];
 
   // A key/value head's split of the prefix is read by all its row tiles: neighbours in
   // this order, which is dealt to the XCDs in eight pieces.
   const unsigned total = (unsigned)a.row_tiles * (unsigned)a.nkv * (unsigned)a.prefix_splits;
-  const unsigned piece = (total + kXcds - 1) / kXcds;
-  const unsigned id = (blockIdx.x % kXcds) * piece + blockIdx.x / kXcds;
+  const unsigned per_xcd = (total + kXcds - 1) / kXcds;
+  const unsigned id = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
   if (id >= total) return;
   int tile = (int)(id % (unsigned)a.row_tiles);
   const unsigned pair = id / (unsigned)a.row_tiles;
@@ -158,84 +176,102 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
 
   // Tile to registers, registers to LDS. A thread's chunks lie one after another in
   // rows of the tile, a wave's in whole rows of one 16-token piece and so of one page.
+  // The places of 64 pieces at a time are kept in the lanes of a register, so that a
+  // piece costs a wave two lane reads and its page's division is one in 64.
+  constexpr int RP = NT / RC;                        // rows of a pass of all threads
+  constexpr int TP = TN / kTile;                     // pieces of a tile
   const int c0 = (int)threadIdx.x % RC;
-  u32x4 kr[CH], vr[CH];
-  uint32_t ks[CH], vs[CH];
-  bool live[CH];
-  auto load_tile = [&](int t) {
+  const int my_row = (int)threadIdx.x / RC;          // of the first pass
+  const int lane_row = my_row & (kTile - 1);
+  const int w_piece = w * (64 / RC) / kTile;         // of the wave's rows in a pass
+  struct Places {
+    int64_t at, scale_at;                            // of this lane's piece
+    uint64_t ok;                                     // the pieces that are in the cache
+  };
+  auto page_of = [&](int t) {                        // of this lane's piece of 64 from t on
+    const int tp = t + lane * kTile;
+    return tp < t_hi ? table[tp / a.block_size] : -1;
+  };
+  auto places = [&](int t, int page, const PagedCache& c, const PagedCacheFp8& c8) {
+    Places x;
+    const int in = (t + lane * kTile) % a.block_size;
+    const bool ok = page >= 0 && page < a.num_blocks;
+    const int64_t b = ok ? page : 0;
+    x.at = FP8 ? kvh * c8.head_s + b * c8.block_s + in * c8.token_s
+               : kvh * c.head_s + b * c.block_s + in * c.token_s;
+    x.scale_at = FP8 ? kvh * c8.scale_head_s + b * c8.scale_block_s + in : 0;
+    x.ok = __ballot(ok);
+    return x;
+  };
+  auto lane_of = [&](int64_t x, int n) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, n);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), n);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+  };
+  // Chunk i of a thread: the piece it is in, and its row's first in the piece.
+  auto piece = [&](int n, int i) { return n + (RP >= kTile ? i * (RP / kTile) + w_piece : i * RP / kTile); };
+  constexpr auto row_in = [](int i) { return RP >= kTile ? 0 : (i * RP) & (kTile - 1); };
+  // A tile of a bf16 cache goes to LDS past the registers, a wave's 64 chunks to 1 KB in
+  // their order: the lane that fills a place takes the chunk that belongs there.
+  auto copy_tile = [&](const PagedCache& c, const Places& x, int n, bool keys, uint16_t* to) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int row = (i * NT + (int)threadIdx.x) / RC;                  // in the tile
-      const int piece16 = ((i * NT + w * 64) / RC) & ~(kTile - 1);       // uniform
-      const int tp = t + piece16;
-      const int b = tp / a.block_size;
-      const int pg = tp < t_hi ? table[b] : -1;
-      const bool ok = pg >= 0 && pg < a.num_blocks;
-      live[i] = ok && t + row < t_hi;
-      const int64_t page = ok ? pg : 0;
-      const int in = tp - b * a.block_size + (row & (kTile - 1));
-      if constexpr (FP8) {
-        const uint8_t* kp = (const uint8_t*)a.kc8.p + (int64_t)kvh * a.kc8.head_s + page * a.kc8.block_s;
-        const uint8_t* vp = (const uint8_t*)a.vc8.p + (int64_t)kvh * a.vc8.head_s + page * a.vc8.block_s;
-        const uint2 x = *(const uint2*)(kp + (int64_t)in * a.kc8.token_s + c0 * 8);
-        const uint2 y = *(const uint2*)(vp + (int64_t)in * a.vc8.token_s + c0 * 8);
-        kr[i] = u32x4{x.x, x.y, 0, 0};
-        vr[i] = u32x4{y.x, y.y, 0, 0};
-        ks[i] = a.kc8.scale[page * a.kc8.scale_block_s + kvh * a.kc8.scale_head_s + in];
-        vs[i] = a.vc8.scale[page * a.vc8.scale_block_s + kvh * a.vc8.scale_head_s + in];
-      } else {
-        const uint16_t* kp = (const uint16_t*)a.kc.p + (int64_t)kvh * a.kc.head_s + page * a.kc.block_s;
-        const uint16_t* vp = (const uint16_t*)a.vc.p + (int64_t)kvh * a.vc.head_s + page * a.vc.block_s;
-        kr[i] = ld16(kp + (int64_t)in * a.kc.token_s + c0 * 8);
-        vr[i] = ld16(vp + (int64_t)in * a.vc.token_s + c0 * 8);
-      }
+      const int row = row_in(i) + lane_row;
+      const int ch = keys ? key_chunk<HD>(row, c0) : value_chunk<HD>(row, c0);
+      // from the piece's start, so that a lane's offset has 32 bits (token strides are checked)
+      copy_to_lds((uint16_t*)c.p + lane_of(x.at, piece(n, i)), (row * (int)c.token_s + ch * 8) * 2,
+                  to + (i * NT + w * 64) * 8);
     }
   };
-  auto store_tile = [&](int buf, int t) {
+  // Codes of a quantised one pass through registers and are widened there.
+  constexpr int CR = FP8 ? CH : 1;
+  uint2 kr[CR], vr[CR];
+  uint32_t ks[CR], vs[CR];
+  auto load_codes = [&](const PagedCacheFp8& c, const Places& x, int n, uint2* to, uint32_t* scale) {
+#pragma unroll
+    for (int i = 0; i < CR; ++i) {
+      const int row = row_in(i) + lane_row;
+      to[i] = *(const uint2*)((const uint8_t*)c.p + lane_of(x.at, piece(n, i)) + ((int64_t)row * c.token_s + c0 * 8));
+      scale[i] = c.scale[lane_of(x.scale_at, piece(n, i)) + row];
+    }
+  };
+  auto store_codes = [&](uint16_t* to, bool keys, const uint2* from, const uint32_t* scale) {
+#pragma unroll
+    for (int i = 0; i < CR; ++i) {
+      const int row = i * RP + my_row;
+      const int ch = keys ? key_chunk<HD>(row, c0) : value_chunk<HD>(row, c0);
+      st16(to + row * HD + ch * 8, fp8_to_bf16(from[i].x, from[i].y, scale_float(scale[i])));
+    }
+  };
+  // Values of tokens that no row sees count as zeros: a weight of 0 would not undo an
+  // infinity or a NaN. `seen`: the tile's pieces that are in the cache.
+  constexpr uint32_t kWhole = (1u << TP) - 1;
+  auto clear_v = [&](uint16_t* V, int t, uint32_t seen) {
+    if (t + TN <= t_hi && seen == kWhole) return;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int row = (i * NT + (int)threadIdx.x) / RC;
-      u32x4 k = kr[i], v = vr[i];
-      if constexpr (FP8) {
-        k = fp8_to_bf16(k[0], k[1], scale_float(ks[i]));
-        v = fp8_to_bf16(v[0], v[1], scale_float(vs[i]));
-      }
-      // values of tokens that no row sees count as zeros: a weight of 0 would not
-      // undo an infinity or a NaN
-      if (!live[i]) v = u32x4{0, 0, 0, 0};
-      const int at = row * HD + chunk_at<HD>(row, c0) * 8;
-      st16(&Kl[buf][at], k);
-      st16(&Vl[buf][at], v);
-      if ((row & (kTile - 1)) == 0 && c0 == 0) live_s[buf][row / kTile] = live[i];
+      const int row = i * RP + my_row;
+      if (t + row >= t_hi || !(seen >> (row / kTile) & 1)) st16(V + row * HD + c0 * 8, u32x4{0, 0, 0, 0});
     }
   };
 
   float m = kNone, l = 0.f;
-  f32x16 O[DB];
+  f32x16 O[DB], S0[TB], S1[TB];
 #pragma unroll
   for (int d = 0; d < DB; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) O[d][i] = 0.f;
 
   // where this lane reads: keys by row, values four tokens by sixteen columns
-  int k_at[KS], v_at[DB];
-#pragma unroll
-  for (int s = 0; s < KS; ++s) k_at[s] = l32 * HD + chunk_at<HD>(l32, 2 * s + half) * 8;
+  // (step s's chunk of a key row, 2 s + half dealt, is that of step 0 with 2 s flipped)
+  const int k_at = l32 * HD + key_chunk<HD>(l32, half) * 8;
+  int v_at[DB];
   const int v_row = half * 4 + (lane >> 2 & 3);
 #pragma unroll
   for (int d = 0; d < DB; ++d)
-    v_at[d] = v_row * HD + chunk_at<HD>(v_row, d * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1)) * 8 + (lane & 1) * 4;
+    v_at[d] = v_row * HD + value_chunk<HD>(v_row, d * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1)) * 8 + (lane & 1) * 4;
 
-  auto compute = [&](int buf, int t) {
-    const uint16_t* const K = Kl[buf];
-    const uint16_t* const V = Vl[buf];
-    bool whole = t + TN <= t_hi;
-    uint32_t seen = 0;
-#pragma unroll
-    for (int x = 0; x < TN / kTile; ++x) seen |= (live_s[buf][x] ? 1u : 0u) << x;
-    seen = __builtin_amdgcn_readfirstlane((int)seen);
-    whole = whole && seen == (1u << (TN / kTile)) - 1;
-    f32x16 s[TB];
+  auto scores = [&](const uint16_t* K, f32x16* s) {
 #pragma unroll
     for (int b = 0; b < TB; ++b)
 #pragma unroll
@@ -245,23 +281,31 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
 #pragma unroll
       for (int b = 0; b < TB; ++b)
         s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            __builtin_bit_cast(bf16x8, ld16(K + k_at[x] + b * 32 * HD)),
+            __builtin_bit_cast(bf16x8, ld16(K + (k_at ^ x * 16) + b * 32 * HD)),
             __builtin_bit_cast(bf16x8, qf[x]), s[b], 0, 0, 0);
-    if (!whole) {
+  };
+  // scores of tokens behind the split's end or in pages outside the cache
+  auto mask = [&](int t, uint32_t seen, f32x16* s) {
 #pragma unroll
-      for (int b = 0; b < TB; ++b)
+    for (int b = 0; b < TB; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int at = b * 32 + (i >> 2) * 8 + half * 4 + (i & 3);
-          if (t + at >= t_hi || !(seen >> (at / kTile) & 1)) s[b][i] = -INFINITY;
-        }
-    }
-    float top = s[0][0];
+      for (int i = 0; i < 16; ++i) {
+        const int at = b * 32 + (i >> 2) * 8 + half * 4 + (i & 3);
+        if (t + at >= t_hi || !(seen >> (at / kTile) & 1)) s[b][i] = -INFINITY;
+      }
+  };
+  auto largest = [&](const f32x16* s) {
+    float top = kNone;
 #pragma unroll
     for (int b = 0; b < TB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-    top = fmaxf(top, __shfl_xor(top, 32)) * c;
+    return top;
+  };
+  // the running maximum takes in a tile's scores
+  auto take_max = [&](float top) {
+    const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+    top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * c;
     if (__any(top > m + kSlack)) {
       const float mn = fmaxf(m, top);
       const float f = exp2_(m - mn);
@@ -272,39 +316,181 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[d][i] *= f;
     }
-    uint32_t p[TB * 8];
+  };
+  constexpr int NW = TB * 8;                          // words of a tile's weights, two in each
+  auto weight = [&](const f32x16* s, uint32_t* p, int x) {
+    const float p0 = exp2_(fmaf(s[x / 8][x % 8 * 2], c, -m)), p1 = exp2_(fmaf(s[x / 8][x % 8 * 2 + 1], c, -m));
+    p[x] = pack_bf16(p0, p1);
+    l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p[x]),
+                                        __builtin_bit_cast(bf16x2, 0x3F803F80u), l, false);
+  };
+  // Both products of a turn, the scores of the next tile (keys Kn) and the values of this one
+  // (V) under its weights, step by step in the order in which they are to be issued: a
+  // matrix instruction, the LDS read that a later one needs, and a share of the
+  // exponentials, which run beside it. The maximum of the next scores is returned.
+  auto products = [&](const uint16_t* Kn, const uint16_t* V, const f32x16* cur, f32x16* next) {
+    constexpr int NQ = KS * TB, NV = TB * 2 * DB, AHEAD = 4;
+    u32x4 kf[AHEAD];
+    struct Columns { s16x4 a, b; } vf[AHEAD];
+    uint32_t p[NW];
+    int k_lane = k_at;
+    asm volatile("" : "+v"(k_lane));                  // its steps are made anew, not kept in registers
+    auto read_k = [&](int n) { return ld16(Kn + (k_lane ^ n / TB * 16) + n % TB * 32 * HD); };
+    auto read_v = [&](int n) {
+      typedef __attribute__((address_space(3))) s16x4 lds4;
+      const uint16_t* at = V + v_at[n % DB] + n / DB * 16 * HD;
+      return Columns{__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)at),
+                     __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 8 * HD))};
+    };
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) kf[n] = read_k(n);
 #pragma unroll
     for (int b = 0; b < TB; ++b)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[b * 8 + i] = pack_bf16(exp2_(fmaf(s[b][2 * i], c, -m)), exp2_(fmaf(s[b][2 * i + 1], c, -m)));
-        l += __uint_as_float(p[b * 8 + i] << 16) + __uint_as_float(p[b * 8 + i] & 0xFFFF0000u);
-      }
+      for (int i = 0; i < 16; ++i) next[b][i] = 0.f;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int x = 0; x < TN / 16; ++x) {
-      const u32x4 pf = {p[x * 4], p[x * 4 + 1], p[x * 4 + 2], p[x * 4 + 3]};
+    for (int n = 0; n < NQ; ++n) {
+      next[n % TB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          __builtin_bit_cast(bf16x8, kf[n % AHEAD]), __builtin_bit_cast(bf16x8, qf[n / TB]), next[n % TB], 0, 0, 0);
+      if (n + AHEAD < NQ) kf[n % AHEAD] = read_k(n + AHEAD);
+      else vf[n + AHEAD - NQ] = read_v(n + AHEAD - NQ);
 #pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        typedef __attribute__((address_space(3))) s16x4 lds4;
-        const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(V + v_at[d] + x * 16 * HD));
-        const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(V + v_at[d] + (x * 16 + 8) * HD));
-        struct { s16x4 a, b; } v = {v0, v1};
-        O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
-                                                       __builtin_bit_cast(bf16x8, pf), O[d], 0, 0, 0);
-      }
+      for (int x = n * (NW / 2) / NQ; x < (n + 1) * (NW / 2) / NQ; ++x) weight(cur, p, x);
+      asm volatile("" : "+v"(l));                     // the sums stay in their step
+      __builtin_amdgcn_sched_barrier(0);
     }
+    float top = kNone;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const u32x4 pf = {p[n / DB * 4], p[n / DB * 4 + 1], p[n / DB * 4 + 2], p[n / DB * 4 + 3]};
+      O[n % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[n % AHEAD]),
+                                                         __builtin_bit_cast(bf16x8, pf), O[n % DB], 0, 0, 0);
+      if (n + AHEAD < NV) vf[n % AHEAD] = read_v(n + AHEAD);
+      if (n < NV / 2) {
+#pragma unroll
+        for (int x = n * NW / NV; x < (n + 1) * NW / NV; ++x) weight(cur, p, NW / 2 + x);
+      } else {
+#pragma unroll
+        for (int x = (n - NV / 2) * NW * 4 / NV; x < (n - NV / 2 + 1) * NW * 4 / NV; ++x)
+          top = fmaxf(top, next[x / 16][x % 16]);
+      }
+      asm volatile("" : "+v"(l), "+v"(top));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    return top;
   };
 
-  load_tile(t_lo);
-  store_tile(0, t_lo);
+  // Scores run a tile ahead of their weights, so that the first product of the next tile
+  // and the exponentials of this one have no order between them. In the turn of tile x,
+  // keys of tile x + 2 and values of x + 1 go to LDS; codes were requested a turn before.
+  constexpr int kSpan = 64 * kTile;                   // tokens that have their places in lanes
+  int next_page = page_of(t_lo);
+  Places pk = places(t_lo, next_page, a.kc, a.kc8), pv = places(t_lo, next_page, a.vc, a.vc8);
+  next_page = page_of(t_lo + kSpan);
+  auto piece_at = [&](int t) { return (t - t_lo) / kTile & 63; };
+  auto seen_at = [&](const Places& x, int t) { return (uint32_t)(x.ok >> piece_at(t)) & kWhole; };
+  // requests of codes, or copies, of tile t; the places of 64 pieces begin with one of them
+  auto ask_k = [&](int t, uint16_t* to) {
+    if (piece_at(t) == 0 && t > t_lo) pk = places(t, next_page, a.kc, a.kc8);
+    if constexpr (FP8) load_codes(a.kc8, pk, piece_at(t), kr, ks);
+    else copy_tile(a.kc, pk, piece_at(t), true, to);
+  };
+  auto ask_v = [&](int t, uint16_t* to) {
+    if (piece_at(t) == 0 && t > t_lo) {
+      pv = places(t, next_page, a.vc, a.vc8);
+      next_page = page_of(t + kSpan);                 // the keys have had theirs, a turn ago
+    }
+    if constexpr (FP8) load_codes(a.vc8, pv, piece_at(t), vr, vs);
+    else copy_tile(a.vc, pv, piece_at(t), false, to);
+  };
+  // the pieces there are: of the next tile's keys, of those after it, of the next values
+  uint32_t k_seen1 = seen_at(pk, t_lo + TN), k_seen2 = 0, v_seen1 = 0;
+  ask_k(t_lo, K0);
+  ask_v(t_lo, V0);
+  if constexpr (FP8) {
+    store_codes(K0, true, kr, ks);
+    store_codes(V0, false, vr, vs);
+  } else {
+    __builtin_amdgcn_s_waitcnt(0x0f70);               // vmcnt(0)
+  }
+  clear_v(V0, t_lo, seen_at(pk, t_lo));
+  if (t_lo + TN < t_hi) {
+    ask_k(t_lo + TN, K1);
+    if constexpr (FP8) {
+      store_codes(K1, true, kr, ks);
+      ask_v(t_lo + TN, nullptr);
+      v_seen1 = seen_at(pv, t_lo + TN);
+      if (t_lo + 2 * TN < t_hi) {
+        ask_k(t_lo + 2 * TN, nullptr);
+        k_seen2 = seen_at(pk, t_lo + 2 * TN);
+      }
+    } else {
+      __builtin_amdgcn_s_waitcnt(0x0f70);
+    }
+  }
   __syncthreads();
-  int buf = 0;
-  for (int t = t_lo; t < t_hi; t += TN, buf ^= 1) {
-    const bool more = t + TN < t_hi;
-    if (more) load_tile(t + TN);
-    if (busy) compute(buf, t);
-    if (more) store_tile(buf ^ 1, t + TN);
+  if (busy) {
+    scores(K0, S0);
+    if (t_lo + TN > t_hi || seen_at(pk, t_lo) != kWhole) mask(t_lo, seen_at(pk, t_lo), S0);
+    take_max(largest(S0));
+  }
+  __syncthreads();                                    // the first tile's keys have been read
+
+  // Tile t: its scores are in `cur`, its values in V; the next one's keys in Kn. The scores
+  // of the next one are made whether there is one or not.
+  auto turn = [&](int t, uint16_t* K, uint16_t* Kn, uint16_t* V, uint16_t* Vn, f32x16* cur,
+                  f32x16* next) {
+    const bool more = t + TN < t_hi, more2 = t + 2 * TN < t_hi;
+    uint32_t k_seen3 = 0, v_seen2 = 0;
+    if constexpr (FP8) {
+      if (more2) store_codes(K, true, kr, ks);
+      if (more) {
+        store_codes(Vn, false, vr, vs);
+        clear_v(Vn, t + TN, v_seen1);
+      }
+      if (t + 3 * TN < t_hi) {
+        ask_k(t + 3 * TN, nullptr);
+        k_seen3 = seen_at(pk, t + 3 * TN);
+      }
+      if (more2) {
+        ask_v(t + 2 * TN, nullptr);
+        v_seen2 = seen_at(pv, t + 2 * TN);
+      }
+    } else {
+      if (more2) {
+        ask_k(t + 2 * TN, K);
+        k_seen2 = seen_at(pk, t + 2 * TN);
+      }
+      if (more) {
+        ask_v(t + TN, Vn);
+        v_seen1 = seen_at(pv, t + TN);
+      }
+    }
+    if (busy) {
+      float top = products(Kn, V, cur, next);
+      if (more) {
+        if (t + 2 * TN > t_hi || k_seen1 != kWhole) {
+          mask(t + TN, k_seen1, next);
+          top = largest(next);
+        }
+        take_max(top);
+      }
+    }
+    if constexpr (!FP8) {
+      __builtin_amdgcn_s_waitcnt(0x0f70);
+      if (more) clear_v(Vn, t + TN, v_seen1);
+    }
+    k_seen1 = k_seen2;
+    k_seen2 = k_seen3;
+    v_seen1 = v_seen2;
     __syncthreads();
+  };
+  for (int t = t_lo;;) {
+    turn(t, K0, K1, V0, V1, S0, S1);
+    if ((t += TN) >= t_hi) break;
+    turn(t, K1, K0, V1, V0, S1, S0);
+    if ((t += TN) >= t_hi) break;
   }
 
   l += __shfl_xor(l, 32);

@@ -236,3 +236,9 @@ def test_read_binding_refuses(change):
     with pytest.raises(ValueError):
         scs.sc_paged_cache_read_fp8(t["k_cache"], t["k_scale"], t["v_cache"], t["v_scale"], k, v,
                                     t["block_table"], starts, first)
+
+
+def test_prefix_token_strides():
+    """Sixteen tokens of a bf16 cache lie within 2^31 bytes."""
+    for which in ("kc", "vc"):
+        assert prefix(attn_desc(), False, **{which: cache(token_stride=1 << 26)}) == UNSUPPORTED
