@@ -546,8 +546,8 @@ sc_status sc_paged_attn_decode_fp8(const sc_paged_attn_desc* desc, const void* q
  * block_table rows hold a request's whole cache, its prefix first. Over the prefix,
  * weights are rounded to bf16 (their sum is of the rounded ones); everything else is
  * as in sc_paged_attn_decode and sc_paged_attn_decode_fp8. Other arguments, limits
- * and alignment are theirs, and bf16 caches have a token stride below 2^26; one
- * workspace function serves both caches. */
+ * and alignment are theirs, and token strides are below 2^26; one workspace function
+ * serves both caches. */
 sc_status sc_paged_attn_prefix_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
                                                int32_t q_len, int32_t max_seq_len,
                                                int32_t num_groups, int32_t max_prefix_len,

@@ -362,7 +362,8 @@ sc_status attn_prefix_call(const sc_paged_attn_desc* desc, const void* q, void* 
                  workspace_bytes, need, &a);
   if (st != SC_OK) return st;
   // a lane's offset in 16 tokens has 32 bits
-  if (!fp8 && (a.kc.token_s >= (1 << 26) || a.vc.token_s >= (1 << 26))) return SC_ERR_UNSUPPORTED;
+  if (std::max({a.kc.token_s, a.vc.token_s, a.kc8.token_s, a.vc8.token_s}) >= (1 << 26))
+    return SC_ERR_UNSUPPORTED;
   a.group_starts = group_start_loc;
   a.prefix_lens = prefix_lens;
   return from_hip(sc::launch_paged_attn_prefix(a, fp8, (hipStream_t)stream));

@@ -23,11 +23,13 @@
 // LDS read brings the values' columns in that order.
 //
 // Matrix instructions and exponentials take about the same time: scores run a tile
-// ahead, and both products' instructions are issued with the exponentials, LDS reads and
-// sums between them. 2,048 rows x 4 key/value heads x 128 on 32,768 tokens: 147 us, 932
-// TFLOP/s (a large bf16 library product reaches 1,158 here); with the compiler's order
-// 187, with this order and tiles through registers 174, with copies that stop the
-// counters of LDS reads 153. 7 us of it are the parts' way to the workspace.
+// ahead, and both products' instructions are issued with the exponentials, LDS reads,
+// sums and the next tiles' copies between them. 2,048 rows x 4 key/value heads x 128 on
+// 32,768 tokens: 148 us, 928 TFLOP/s (a large bf16 library product reaches 1,158 here);
+// with the compiler's order 187, with this order and tiles through registers 174, with
+// copies that stop the counters of LDS reads 153. 7 us of it are the parts' way to the
+// workspace. Matrix units are busy 44% of the cycles; with no LDS reads, copies or barriers at
+// all it takes 116 us, and the clock falls (2.2 to 2.0 GHz) as they get busier.
 //
 // Weights are rounded to bf16 (by 2^-8 of each at most), and the sum is taken of the
 // rounded ones, so that their mean stays one of the values: the error is that of the
@@ -37,11 +39,15 @@
 #include "fp8_device.hpp"
 
 #include <algorithm>
+#include <utility>
 
 namespace sc {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// The kernel's parts are lambdas over its registers: none may become a call.
+#define SC_INLINE __attribute__((always_inline))
 
 namespace {
 
@@ -67,16 +73,38 @@ __device__ __forceinline__ int value_chunk(int row, int c) {
   return c ^ (HD == 64 ? (row >> 1 & 1) * 4 : (row & 3) * 4);
 }
 
+// f(0), f(1), ... f(N - 1) with the numbers as types: what depends on one is settled when
+// it is compiled, so that a sequence of steps stays one block of instructions.
+template <class F, int... I>
+__device__ __forceinline__ void steps_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void steps(F f) {
+  steps_of(f, std::make_integer_sequence<int, N>{});
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   f32x2 p = {x, y};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
 }
 
-// 16 bytes a lane from `bytes` behind `from` (uniform) to LDS, lane after lane. As a buffer
-// access: the counters of LDS reads go on beside it, which a global one stops.
-__device__ __forceinline__ void copy_to_lds(uint16_t* from, int bytes, uint16_t* to) {
-  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(from, (short)0, 0x7FFFFFFF, 0x00020000);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, bytes, 0, 0, 0);
+// Reads from `bytes` behind `from` (uniform), as buffer accesses: a lane's offset has 32
+// bits, nothing is read where `there` is false, and the counters of LDS reads go on
+// beside one that ends in LDS, which a global access stops.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* from, bool there) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(from), (short)0, there ? 0x7FFFFFFF : 0, 0x00020000);
+}
+// 16 bytes a lane to LDS, lane after lane.
+__device__ __forceinline__ void copy_to_lds(const uint16_t* from, int bytes, bool there, uint16_t* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_at(from, there),
+                                           (__attribute__((address_space(3))) void*)to, 16, bytes, 0, 0, 0);
+}
+__device__ __forceinline__ uint2 read_codes(const uint8_t* from, int bytes, bool there) {
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(buffer_at(from, there), bytes, 0, 0));
+}
+__device__ __forceinline__ uint32_t read_scale(const uint8_t* from, int bytes, bool there) {
+  return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(buffer_at(from, there), bytes, 0, 0);
 }
 
 // The group of a row tile and the tile's number in it (-1: there is no such tile).
@@ -188,11 +216,11 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
     int64_t at, scale_at;                            // of this lane's piece
     uint64_t ok;                                     // the pieces that are in the cache
   };
-  auto page_of = [&](int t) {                        // of this lane's piece of 64 from t on
+  auto page_of = [&](int t) SC_INLINE {                        // of this lane's piece of 64 from t on
     const int tp = t + lane * kTile;
     return tp < t_hi ? table[tp / a.block_size] : -1;
   };
-  auto places = [&](int t, int page, const PagedCache& c, const PagedCacheFp8& c8) {
+  auto places = [&](int t, int page, const PagedCache& c, const PagedCacheFp8& c8) SC_INLINE {
     Places x;
     const int in = (t + lane * kTile) % a.block_size;
     const bool ok = page >= 0 && page < a.num_blocks;
@@ -203,50 +231,43 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
     x.ok = __ballot(ok);
     return x;
   };
-  auto lane_of = [&](int64_t x, int n) {
+  auto lane_of = [&](int64_t x, int n) SC_INLINE {
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, n);
     const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), n);
     return (int64_t)((uint64_t)hi << 32 | lo);
   };
   // Chunk i of a thread: the piece it is in, and its row's first in the piece.
-  auto piece = [&](int n, int i) { return n + (RP >= kTile ? i * (RP / kTile) + w_piece : i * RP / kTile); };
+  auto piece = [&](int n, int i) SC_INLINE { return n + (RP >= kTile ? i * (RP / kTile) + w_piece : i * RP / kTile); };
   constexpr auto row_in = [](int i) { return RP >= kTile ? 0 : (i * RP) & (kTile - 1); };
-  // A tile of a bf16 cache goes to LDS past the registers, a wave's 64 chunks to 1 KB in
-  // their order: the lane that fills a place takes the chunk that belongs there.
-  auto copy_tile = [&](const PagedCache& c, const Places& x, int n, bool keys, uint16_t* to) {
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int row = row_in(i) + lane_row;
-      const int ch = keys ? key_chunk<HD>(row, c0) : value_chunk<HD>(row, c0);
-      // from the piece's start, so that a lane's offset has 32 bits (token strides are checked)
-      copy_to_lds((uint16_t*)c.p + lane_of(x.at, piece(n, i)), (row * (int)c.token_s + ch * 8) * 2,
-                  to + (i * NT + w * 64) * 8);
-    }
+  // Chunk i of a tile of a bf16 cache goes to LDS past the registers, a wave's 64 chunks to
+  // 1 KB in their order: the lane that fills a place takes the chunk that belongs there.
+  auto copy_chunk = [&](const PagedCache& c, const Places& x, int n, int i, bool there, bool keys,
+                        uint16_t* to) SC_INLINE {
+    const int row = row_in(i) + lane_row;
+    const int ch = keys ? key_chunk<HD>(row, c0) : value_chunk<HD>(row, c0);
+    // from the piece's start, so that a lane's offset has 32 bits (token strides are checked)
+    copy_to_lds((uint16_t*)c.p + lane_of(x.at, piece(n, i)), (row * (int)c.token_s + ch * 8) * 2,
+                there, to + (i * NT + w * 64) * 8);
   };
   // Codes of a quantised one pass through registers and are widened there.
   constexpr int CR = FP8 ? CH : 1;
   uint2 kr[CR], vr[CR];
   uint32_t ks[CR], vs[CR];
-  auto load_codes = [&](const PagedCacheFp8& c, const Places& x, int n, uint2* to, uint32_t* scale) {
-#pragma unroll
-    for (int i = 0; i < CR; ++i) {
-      const int row = row_in(i) + lane_row;
-      to[i] = *(const uint2*)((const uint8_t*)c.p + lane_of(x.at, piece(n, i)) + ((int64_t)row * c.token_s + c0 * 8));
-      scale[i] = c.scale[lane_of(x.scale_at, piece(n, i)) + row];
-    }
+  auto load_codes = [&](const PagedCacheFp8& c, const Places& x, int n, int i, bool there, uint2& to,
+                        uint32_t& scale) SC_INLINE {
+    const int row = row_in(i) + lane_row;
+    to = read_codes((uint8_t*)c.p + lane_of(x.at, piece(n, i)), row * (int)c.token_s + c0 * 8, there);
+    scale = read_scale(c.scale + lane_of(x.scale_at, piece(n, i)), row, there);
   };
-  auto store_codes = [&](uint16_t* to, bool keys, const uint2* from, const uint32_t* scale) {
-#pragma unroll
-    for (int i = 0; i < CR; ++i) {
-      const int row = i * RP + my_row;
-      const int ch = keys ? key_chunk<HD>(row, c0) : value_chunk<HD>(row, c0);
-      st16(to + row * HD + ch * 8, fp8_to_bf16(from[i].x, from[i].y, scale_float(scale[i])));
-    }
+  auto store_codes = [&](uint16_t* to, int i, bool keys, uint2 from, uint32_t scale) SC_INLINE {
+    const int row = i * RP + my_row;
+    const int ch = keys ? key_chunk<HD>(row, c0) : value_chunk<HD>(row, c0);
+    st16(to + row * HD + ch * 8, fp8_to_bf16(from.x, from.y, scale_float(scale)));
   };
   // Values of tokens that no row sees count as zeros: a weight of 0 would not undo an
   // infinity or a NaN. `seen`: the tile's pieces that are in the cache.
   constexpr uint32_t kWhole = (1u << TP) - 1;
-  auto clear_v = [&](uint16_t* V, int t, uint32_t seen) {
+  auto clear_v = [&](uint16_t* V, int t, uint32_t seen) SC_INLINE {
     if (t + TN <= t_hi && seen == kWhole) return;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -271,7 +292,7 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
   for (int d = 0; d < DB; ++d)
     v_at[d] = v_row * HD + value_chunk<HD>(v_row, d * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1)) * 8 + (lane & 1) * 4;
 
-  auto scores = [&](const uint16_t* K, f32x16* s) {
+  auto scores = [&](const uint16_t* K, f32x16* s) SC_INLINE {
 #pragma unroll
     for (int b = 0; b < TB; ++b)
 #pragma unroll
@@ -285,7 +306,7 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
             __builtin_bit_cast(bf16x8, qf[x]), s[b], 0, 0, 0);
   };
   // scores of tokens behind the split's end or in pages outside the cache
-  auto mask = [&](int t, uint32_t seen, f32x16* s) {
+  auto mask = [&](int t, uint32_t seen, f32x16* s) SC_INLINE {
 #pragma unroll
     for (int b = 0; b < TB; ++b)
 #pragma unroll
@@ -294,7 +315,7 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
         if (t + at >= t_hi || !(seen >> (at / kTile) & 1)) s[b][i] = -INFINITY;
       }
   };
-  auto largest = [&](const f32x16* s) {
+  auto largest = [&](const f32x16* s) SC_INLINE {
     float top = kNone;
 #pragma unroll
     for (int b = 0; b < TB; ++b)
@@ -303,7 +324,7 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
     return top;
   };
   // the running maximum takes in a tile's scores
-  auto take_max = [&](float top) {
+  auto take_max = [&](float top) SC_INLINE {
     const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
     top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * c;
     if (__any(top > m + kSlack)) {
@@ -318,30 +339,45 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
     }
   };
   constexpr int NW = TB * 8;                          // words of a tile's weights, two in each
-  auto weight = [&](const f32x16* s, uint32_t* p, int x) {
-    const float p0 = exp2_(fmaf(s[x / 8][x % 8 * 2], c, -m)), p1 = exp2_(fmaf(s[x / 8][x % 8 * 2 + 1], c, -m));
-    p[x] = pack_bf16(p0, p1);
-    l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p[x]),
-                                        __builtin_bit_cast(bf16x2, 0x3F803F80u), l, false);
+  struct Two { float x, y; };
+  auto exponents = [&](const f32x16* s, int x) SC_INLINE {
+    return Two{fmaf(s[x / 8][x % 8 * 2], c, -m), fmaf(s[x / 8][x % 8 * 2 + 1], c, -m)};
+  };
+  auto sum = [&](uint32_t p) SC_INLINE {
+    l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), __builtin_bit_cast(bf16x2, 0x3F803F80u), l, false);
+  };
+  struct Columns { s16x4 a, b; };
+  auto read_v = [&](const uint16_t* V, int n) SC_INLINE {
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const uint16_t* at = V + v_at[n % DB] + n / DB * 16 * HD;
+    return Columns{__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)at),
+                   __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 8 * HD))};
+  };
+  auto value_step = [&](const Columns& v, const uint32_t* p, int n) SC_INLINE {
+    const u32x4 pf = {p[n / DB * 4], p[n / DB * 4 + 1], p[n / DB * 4 + 2], p[n / DB * 4 + 3]};
+    O[n % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
+                                                       __builtin_bit_cast(bf16x8, pf), O[n % DB], 0, 0, 0);
   };
   // Both products of a turn, the scores of the next tile (keys Kn) and the values of this one
   // (V) under its weights, step by step in the order in which they are to be issued: a
-  // matrix instruction, the LDS read that a later one needs, and a share of the
-  // exponentials, which run beside it. The maximum of the next scores is returned.
-  auto products = [&](const uint16_t* Kn, const uint16_t* V, const f32x16* cur, f32x16* next) {
-    constexpr int NQ = KS * TB, NV = TB * 2 * DB, AHEAD = 4;
+  // matrix instruction, the LDS read that a later one needs, and of the weights the
+  // exponent of one pair, the power of the pair before and the sum of the one before that,
+  // so that no instruction waits for its neighbour. `chore(i)`, of `chores`, is what else a
+  // turn has to do, the next tiles' way to LDS. The maximum of the next scores is returned.
+  auto products = [&](const uint16_t* Kn, const uint16_t* V, const f32x16* cur, f32x16* next, auto chores,
+                      auto chore) SC_INLINE {
+    constexpr int NQ = KS * TB, NV = TB * 2 * DB, AHEAD = 3;
+    // steps that take weights; a pair is done two slots after its own, and in time
+    constexpr int NS = NW + 2, ES = NQ + NV * 5 / 8;
+    static_assert((NW + 1) * ES / NS < NQ + (NW / 4 - 1) * DB && 5 * ES / NS < NQ, "weights before their product");
     u32x4 kf[AHEAD];
-    struct Columns { s16x4 a, b; } vf[AHEAD];
+    Columns vf[AHEAD];
     uint32_t p[NW];
+    Two e[2];
+    float top[2] = {kNone, kNone};
     int k_lane = k_at;
     asm volatile("" : "+v"(k_lane));                  // its steps are made anew, not kept in registers
-    auto read_k = [&](int n) { return ld16(Kn + (k_lane ^ n / TB * 16) + n % TB * 32 * HD); };
-    auto read_v = [&](int n) {
-      typedef __attribute__((address_space(3))) s16x4 lds4;
-      const uint16_t* at = V + v_at[n % DB] + n / DB * 16 * HD;
-      return Columns{__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)at),
-                     __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 8 * HD))};
-    };
+    auto read_k = [&](int n) SC_INLINE { return ld16(Kn + (k_lane ^ n / TB * 16) + n % TB * 32 * HD); };
 #pragma unroll
     for (int n = 0; n < AHEAD; ++n) kf[n] = read_k(n);
 #pragma unroll
@@ -349,36 +385,44 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
 #pragma unroll
       for (int i = 0; i < 16; ++i) next[b][i] = 0.f;
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      next[n % TB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-          __builtin_bit_cast(bf16x8, kf[n % AHEAD]), __builtin_bit_cast(bf16x8, qf[n / TB]), next[n % TB], 0, 0, 0);
-      if (n + AHEAD < NQ) kf[n % AHEAD] = read_k(n + AHEAD);
-      else vf[n + AHEAD - NQ] = read_v(n + AHEAD - NQ);
-#pragma unroll
-      for (int x = n * (NW / 2) / NQ; x < (n + 1) * (NW / 2) / NQ; ++x) weight(cur, p, x);
-      asm volatile("" : "+v"(l));                     // the sums stay in their step
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    float top = kNone;
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const u32x4 pf = {p[n / DB * 4], p[n / DB * 4 + 1], p[n / DB * 4 + 2], p[n / DB * 4 + 3]};
-      O[n % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[n % AHEAD]),
-                                                         __builtin_bit_cast(bf16x8, pf), O[n % DB], 0, 0, 0);
-      if (n + AHEAD < NV) vf[n % AHEAD] = read_v(n + AHEAD);
-      if (n < NV / 2) {
-#pragma unroll
-        for (int x = n * NW / NV; x < (n + 1) * NW / NV; ++x) weight(cur, p, NW / 2 + x);
+    steps<NQ + NV>([&](auto step) SC_INLINE {
+      constexpr int n = step, nv = n - NQ;
+      if constexpr (n < NQ) {
+        next[n % TB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_bit_cast(bf16x8, kf[n % AHEAD]), __builtin_bit_cast(bf16x8, qf[n / TB]), next[n % TB], 0, 0, 0);
+        if constexpr (n + AHEAD < NQ) kf[n % AHEAD] = read_k(n + AHEAD);
+        else vf[n + AHEAD - NQ] = read_v(V, n + AHEAD - NQ);
       } else {
-#pragma unroll
-        for (int x = (n - NV / 2) * NW * 4 / NV; x < (n - NV / 2 + 1) * NW * 4 / NV; ++x)
-          top = fmaxf(top, next[x / 16][x % 16]);
+        value_step(vf[nv % AHEAD], p, nv);
+        if constexpr (nv + AHEAD < NV) vf[nv % AHEAD] = read_v(V, nv + AHEAD);
       }
-      asm volatile("" : "+v"(l), "+v"(top));
+      steps<NS>([&](auto slot) SC_INLINE {
+        constexpr int x = slot;
+        if constexpr (x * ES / NS == n) {
+          if constexpr (x >= 2) {
+            p[x - 2] = pack_bf16(e[x % 2].x, e[x % 2].y);
+            sum(p[x - 2]);
+          }
+          if constexpr (x >= 1 && x <= NW) e[(x - 1) % 2] = Two{exp2_(e[(x - 1) % 2].x), exp2_(e[(x - 1) % 2].y)};
+          if constexpr (x < NW) e[x % 2] = exponents(cur, x);
+        }
+      });
+      if constexpr (nv >= NV / 2) {
+        constexpr int per = TB * 16 * 2 / NV, from = (nv - NV / 2) * per;
+        steps<per>([&](auto i) SC_INLINE {
+          constexpr int x = from + i;
+          top[x / 2 % 2] = fmaxf(top[x / 2 % 2], next[x / 16][x % 16]);
+        });
+      }
+      steps<decltype(chores)::value>([&](auto i) SC_INLINE {
+        if constexpr (1 + i * (NQ + NV / 2) / decltype(chores)::value == n) chore(i);
+      });
+      // sums and maxima stay in their step
+      if constexpr (nv < NV / 2) asm volatile("" : "+v"(l));
+      else asm volatile("" : "+v"(l), "+v"(top[0]), "+v"(top[1]));
       __builtin_amdgcn_sched_barrier(0);
-    }
-    return top;
+    });
+    return fmaxf(top[0], top[1]);
   };
 
   // Scores run a tile ahead of their weights, so that the first product of the next tile
@@ -388,47 +432,48 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
   int next_page = page_of(t_lo);
   Places pk = places(t_lo, next_page, a.kc, a.kc8), pv = places(t_lo, next_page, a.vc, a.vc8);
   next_page = page_of(t_lo + kSpan);
-  auto piece_at = [&](int t) { return (t - t_lo) / kTile & 63; };
-  auto seen_at = [&](const Places& x, int t) { return (uint32_t)(x.ok >> piece_at(t)) & kWhole; };
-  // requests of codes, or copies, of tile t; the places of 64 pieces begin with one of them
-  auto ask_k = [&](int t, uint16_t* to) {
-    if (piece_at(t) == 0 && t > t_lo) pk = places(t, next_page, a.kc, a.kc8);
-    if constexpr (FP8) load_codes(a.kc8, pk, piece_at(t), kr, ks);
-    else copy_tile(a.kc, pk, piece_at(t), true, to);
-  };
-  auto ask_v = [&](int t, uint16_t* to) {
-    if (piece_at(t) == 0 && t > t_lo) {
-      pv = places(t, next_page, a.vc, a.vc8);
-      next_page = page_of(t + kSpan);                 // the keys have had theirs, a turn ago
+  auto piece_at = [&](int t) SC_INLINE { return (t - t_lo) / kTile & 63; };
+  auto seen_at = [&](const Places& x, int t) SC_INLINE { return (uint32_t)(x.ok >> piece_at(t)) & kWhole; };
+  // the places of 64 pieces begin with a tile's; the values follow the keys by a tile
+  auto go_on = [&](int t) SC_INLINE {
+    if (piece_at(t) == 0) pk = places(t, next_page, a.kc, a.kc8);
+    if (piece_at(t - TN) == 0) {
+      pv = places(t - TN, next_page, a.vc, a.vc8);
+      next_page = page_of(t - TN + kSpan);
     }
-    if constexpr (FP8) load_codes(a.vc8, pv, piece_at(t), vr, vs);
-    else copy_tile(a.vc, pv, piece_at(t), false, to);
   };
-  // the pieces there are: of the next tile's keys, of those after it, of the next values
-  uint32_t k_seen1 = seen_at(pk, t_lo + TN), k_seen2 = 0, v_seen1 = 0;
-  ask_k(t_lo, K0);
-  ask_v(t_lo, V0);
-  if constexpr (FP8) {
-    store_codes(K0, true, kr, ks);
-    store_codes(V0, false, vr, vs);
-  } else {
-    __builtin_amdgcn_s_waitcnt(0x0f70);               // vmcnt(0)
-  }
-  clear_v(V0, t_lo, seen_at(pk, t_lo));
-  if (t_lo + TN < t_hi) {
-    ask_k(t_lo + TN, K1);
+  auto fetch_k = [&](int t, int i, uint16_t* to) SC_INLINE {
+    if constexpr (FP8) load_codes(a.kc8, pk, piece_at(t), i, t < t_hi, kr[i], ks[i]);
+    else copy_chunk(a.kc, pk, piece_at(t), i, t < t_hi, true, to);
+  };
+  auto fetch_v = [&](int t, int i, uint16_t* to) SC_INLINE {
+    if constexpr (FP8) load_codes(a.vc8, pv, piece_at(t), i, t < t_hi, vr[i], vs[i]);
+    else copy_chunk(a.vc, pv, piece_at(t), i, t < t_hi, false, to);
+  };
+  // pieces there are: of the next keys, of those after them, of the next values
+  uint32_t k_seen1 = seen_at(pk, t_lo + TN), k_seen2 = seen_at(pk, t_lo + 2 * TN), v_seen1 = k_seen1;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    fetch_k(t_lo, i, K0);
+    fetch_v(t_lo, i, V0);
     if constexpr (FP8) {
-      store_codes(K1, true, kr, ks);
-      ask_v(t_lo + TN, nullptr);
-      v_seen1 = seen_at(pv, t_lo + TN);
-      if (t_lo + 2 * TN < t_hi) {
-        ask_k(t_lo + 2 * TN, nullptr);
-        k_seen2 = seen_at(pk, t_lo + 2 * TN);
-      }
-    } else {
-      __builtin_amdgcn_s_waitcnt(0x0f70);
+      store_codes(K0, i, true, kr[i], ks[i]);
+      store_codes(V0, i, false, vr[i], vs[i]);
     }
   }
+  if (t_lo + TN < t_hi) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      fetch_k(t_lo + TN, i, K1);
+      if constexpr (FP8) {
+        store_codes(K1, i, true, kr[i], ks[i]);
+        fetch_k(t_lo + 2 * TN, i, nullptr);
+        fetch_v(t_lo + TN, i, nullptr);
+      }
+    }
+  }
+  if constexpr (!FP8) __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+  clear_v(V0, t_lo, seen_at(pk, t_lo));
   __syncthreads();
   if (busy) {
     scores(K0, S0);
@@ -437,61 +482,58 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
   }
   __syncthreads();                                    // the first tile's keys have been read
 
-  // Tile t: its scores are in `cur`, its values in V; the next one's keys in Kn. The scores
-  // of the next one are made whether there is one or not.
-  auto turn = [&](int t, uint16_t* K, uint16_t* Kn, uint16_t* V, uint16_t* Vn, f32x16* cur,
-                  f32x16* next) {
-    const bool more = t + TN < t_hi, more2 = t + 2 * TN < t_hi;
-    uint32_t k_seen3 = 0, v_seen2 = 0;
-    if constexpr (FP8) {
-      if (more2) store_codes(K, true, kr, ks);
-      if (more) {
-        store_codes(Vn, false, vr, vs);
-        clear_v(Vn, t + TN, v_seen1);
-      }
-      if (t + 3 * TN < t_hi) {
-        ask_k(t + 3 * TN, nullptr);
-        k_seen3 = seen_at(pk, t + 3 * TN);
-      }
-      if (more2) {
-        ask_v(t + 2 * TN, nullptr);
-        v_seen2 = seen_at(pv, t + 2 * TN);
-      }
-    } else {
-      if (more2) {
-        ask_k(t + 2 * TN, K);
-        k_seen2 = seen_at(pk, t + 2 * TN);
-      }
-      if (more) {
-        ask_v(t + TN, Vn);
-        v_seen1 = seen_at(pv, t + TN);
-      }
-    }
-    if (busy) {
-      float top = products(Kn, V, cur, next);
-      if (more) {
+  // Tile t: its scores are in `cur`, its values in V; the next one's keys in Kn. What
+  // belongs to tiles behind the last one is done all the same, so that a turn has no
+  // branches, but for their reads.
+  // A wave without rows takes its share in the fetching alone.
+  auto turn = [&](auto idle, int t, uint16_t* K, uint16_t* Kn, uint16_t* V, uint16_t* Vn, f32x16* cur,
+                  f32x16* next) SC_INLINE {
+    constexpr std::integral_constant<int, (FP8 ? 4 : 2) * CH> chores{};
+    auto chore = [&](auto which) SC_INLINE {
+      constexpr int i = which, j = i % CH;
+      if constexpr (FP8 && i < CH) store_codes(Vn, j, false, vr[j], vs[j]);
+      else if constexpr (FP8 && i < 2 * CH) store_codes(K, j, true, kr[j], ks[j]);
+      else if constexpr (FP8 && i < 3 * CH) fetch_v(t + 2 * TN, j, nullptr);
+      else if constexpr (FP8) fetch_k(t + 3 * TN, j, nullptr);
+      else if constexpr (i < CH) fetch_v(t + TN, j, Vn);
+      else fetch_k(t + 2 * TN, j, K);
+    };
+    const uint32_t v_seen2 = FP8 ? seen_at(pv, t + 2 * TN) : seen_at(pv, t + TN);
+    const uint32_t k_seen3 = FP8 ? seen_at(pk, t + 3 * TN) : seen_at(pk, t + 2 * TN);
+    if (!FP8) k_seen2 = k_seen3, v_seen1 = v_seen2;
+    if constexpr (!idle) {
+      float top = products(Kn, V, cur, next, chores, chore);
+      if (t + TN < t_hi) {
         if (t + 2 * TN > t_hi || k_seen1 != kWhole) {
           mask(t + TN, k_seen1, next);
           top = largest(next);
         }
         take_max(top);
       }
+    } else {
+      steps<chores>(chore);
     }
-    if constexpr (!FP8) {
-      __builtin_amdgcn_s_waitcnt(0x0f70);
-      if (more) clear_v(Vn, t + TN, v_seen1);
-    }
+    go_on(t + (FP8 ? 4 : 3) * TN);
+    if constexpr (!FP8) __builtin_amdgcn_s_waitcnt(0x0f70);
+    if (t + TN < t_hi) clear_v(Vn, t + TN, v_seen1);
     k_seen1 = k_seen2;
     k_seen2 = k_seen3;
     v_seen1 = v_seen2;
     __syncthreads();
   };
-  for (int t = t_lo;;) {
-    turn(t, K0, K1, V0, V1, S0, S1);
-    if ((t += TN) >= t_hi) break;
-    turn(t, K1, K0, V1, V0, S1, S0);
-    if ((t += TN) >= t_hi) break;
+  auto turns = [&](auto idle) SC_INLINE {
+    for (int t = t_lo;;) {
+      turn(idle, t, K0, K1, V0, V1, S0, S1);
+      if ((t += TN) >= t_hi) break;
+      turn(idle, t, K1, K0, V1, V0, S1, S0);
+      if ((t += TN) >= t_hi) break;
+    }
+  };
+  if (!busy) {
+    turns(std::true_type{});
+    return;
   }
+  turns(std::false_type{});
 
   l += __shfl_xor(l, 32);
   if (!row_ok) return;

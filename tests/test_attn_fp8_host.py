@@ -239,6 +239,7 @@ def test_read_binding_refuses(change):
 
 
 def test_prefix_token_strides():
-    """Sixteen tokens of a bf16 cache lie within 2^31 bytes."""
+    """Sixteen tokens of a cache lie within 2^31 bytes."""
     for which in ("kc", "vc"):
         assert prefix(attn_desc(), False, **{which: cache(token_stride=1 << 26)}) == UNSUPPORTED
+        assert prefix(attn_desc(), True, **{which: q8(token_stride=1 << 26)}) == UNSUPPORTED
