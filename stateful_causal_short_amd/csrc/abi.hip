@@ -266,7 +266,7 @@ sc_status attn_sizes(const sc_paged_attn_desc* d, int32_t batch, int32_t q_len,
 // The same of an attention call with shared prefixes.
 sc_status prefix_sizes(const sc_paged_attn_desc* d, int32_t batch, int32_t q_len,
                        int32_t max_seq_len, int32_t num_groups, int32_t max_prefix_len,
-                       sc::PagedAttnArgs* a, int64_t* need) {
+                       bool fp8, sc::PagedAttnArgs* a, int64_t* need) {
   if (batch < 0 || q_len < 0 || max_seq_len < 0 || num_groups < 0 || max_prefix_len < 0 ||
       max_prefix_len > max_seq_len)
     return SC_ERR_INVALID_ARG;
@@ -279,7 +279,7 @@ sc_status prefix_sizes(const sc_paged_attn_desc* d, int32_t batch, int32_t q_len
   attn_fill(d, batch, q_len, max_seq_len, a);
   a->groups = num_groups;
   a->max_prefix = num_groups > 0 ? max_prefix_len : 0;
-  const int64_t bytes = sc::plan_paged_attn_prefix(a);
+  const int64_t bytes = sc::plan_paged_attn_prefix(a, fp8);
   if (bytes < 0) return SC_ERR_UNSUPPORTED;
   *need = bytes;
   return SC_OK;
@@ -353,7 +353,7 @@ sc_status attn_prefix_call(const sc_paged_attn_desc* desc, const void* q, void* 
   if (st != SC_OK) return st;
   sc::PagedAttnArgs a;
   int64_t need = 0;
-  st = prefix_sizes(desc, batch, q_len, max_seq_len, num_groups, max_prefix_len, &a, &need);
+  st = prefix_sizes(desc, batch, q_len, max_seq_len, num_groups, max_prefix_len, fp8, &a, &need);
   if (st != SC_OK) return st;
   if ((st = attn_bounds(desc, max_blocks, max_seq_len, workspace_bytes)) != SC_OK) return st;
   if (batch == 0 || q_len == 0) return SC_OK;
@@ -993,10 +993,17 @@ sc_status sc_paged_attn_prefix_workspace_bytes(const sc_paged_attn_desc* desc, i
                                                int32_t num_groups, int32_t max_prefix_len,
                                                int64_t* bytes) {
   if (!desc || !bytes) return SC_ERR_NULL_ARG;
-  const sc_status st = check_attn_desc(desc);
+  sc_status st = check_attn_desc(desc);
   if (st != SC_OK) return st;
+  // what either cache needs
   sc::PagedAttnArgs a;
-  return prefix_sizes(desc, batch, q_len, max_seq_len, num_groups, max_prefix_len, &a, bytes);
+  int64_t need[2];
+  for (int fp8 = 0; fp8 < 2; ++fp8) {
+    st = prefix_sizes(desc, batch, q_len, max_seq_len, num_groups, max_prefix_len, fp8 != 0, &a, &need[fp8]);
+    if (st != SC_OK) return st;
+  }
+  *bytes = std::max(need[0], need[1]);
+  return SC_OK;
 }
 
 sc_status sc_paged_attn_prefix(const sc_paged_attn_desc* desc, const void* q, void* out,

@@ -48,9 +48,10 @@ using ValueRun = uint32_t __attribute__((ext_vector_type(N / 2)));
 }  // namespace
 
 // AFTER: the call's second half behind attn_prefix. A request's tiles begin where
-// its shared tokens end (inside a tile or not), its splits are equal parts of what
-// is left, and the parts go behind the prefix's in the workspace.
-template <int HD, bool AFTER>
+// its shared tokens end (inside a tile or not), and its splits are equal parts of what
+// is left. With kParts they go behind the prefix's parts in the workspace; with kWhole
+// there is one, which takes those in and is done.
+template <int HD, After AFTER>
 __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAttnArgs a) {
   constexpr int KS = HD / 32;               // score products per tile
   constexpr int VPL = HD / 16;              // values of a token's row per lane
@@ -68,13 +69,13 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
   id /= (unsigned)a.batch;
   const int rg = (int)(id % (unsigned)row_groups);
   const int split = (int)(id / (unsigned)row_groups);
-  if (!AFTER && a.sorted) r = by_length(a, r);
+  if (AFTER == After::kNo && a.sorted) r = by_length(a, r);
 
   const int lane = (int)(threadIdx.x & 63);
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l16 = lane & 15, lg = lane >> 4;
   int start = 0, split_len = a.split_len;
-  if constexpr (AFTER) {
+  if constexpr (AFTER != After::kNo) {
     const int len = min(max(a.lens[r], 0), a.max_len);
     start = shared_tokens(a, r, len);
     split_len = own_split_len(a, start, len, 4 * kTile);
@@ -162,7 +163,7 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + lg * 4 + i;
       // positions behind the tile's last visible one hold anything, NaN included
-      s[i] = cur.ok && t <= limit && t < t_hi && (!AFTER || t >= start) ? s[i] * c : -INFINITY;
+      s[i] = cur.ok && t <= limit && t < t_hi && (AFTER == After::kNo || t >= start) ? s[i] * c : -INFINITY;
       top = fmaxf(top, s[i]);
     }
     top = fmaxf(top, __shfl_xor(top, 16));
@@ -206,7 +207,7 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + lg * 4 + i;
-      const bool live = cur.ok && t < t_hi && (!AFTER || t >= start);
+      const bool live = cur.ok && t < t_hi && (AFTER == After::kNo || t >= start);
 #pragma unroll
       for (int u = 0; u < VW; ++u) {
 #pragma unroll
@@ -246,6 +247,9 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
       }
     }
   }
+  if constexpr (AFTER == After::kWhole)
+    take_prefix<HD, VR, VW>(a, r, kvh, rg * kRows, w,
+                       start > 0 ? (start + a.prefix_split_len - 1) / a.prefix_split_len : 0, m, l, O);
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
   // join the four waves: wave 0 takes in the others' parts. O[u VR + e] of a
@@ -275,11 +279,11 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : 4) void attn_split(PagedAtt
     fx[x] = exp2_(ml[x][l16] - mt);
     lt += ll[x][l16] * fx[x];
   }
-  const bool parts = AFTER || a.splits > 1;
+  const bool parts = AFTER == After::kParts || (AFTER == After::kNo && a.splits > 1);
   const float inv = parts ? 1.f : (lt > 0.f ? 1.f / lt : 0.f);
   const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
-  const int row_parts = AFTER ? a.prefix_splits + a.splits : a.splits;
-  const int my_part = AFTER ? a.prefix_splits + split : split;
+  const int row_parts = AFTER != After::kNo ? a.prefix_splits + a.splits : a.splits;
+  const int my_part = AFTER != After::kNo ? a.prefix_splits + split : split;
   float* const wo = a.ws + values_at(n_rows * row_parts);
   const int64_t part = (q_row * a.nq + head) * row_parts + my_part;
   if (parts && row_ok && lg == 0) {
@@ -405,15 +409,21 @@ int64_t own_attn_grid(const PagedAttnArgs& a) {
   return (int64_t)a.batch * a.nkv * ((rows + kRows - 1) / kRows) * a.splits;
 }
 
-// Requests' own tokens behind their shared prefix, into the workspace.
-hipError_t launch_paged_attn_after(const PagedAttnArgs& a, hipStream_t s) {
+namespace {
+template <After AFTER>
+hipError_t launch_after(const PagedAttnArgs& a, hipStream_t s) {
   const int64_t grid = own_attn_grid(a);
   if (grid > 0x7FFFFFFFLL) return hipErrorNotSupported;
   const dim3 g((unsigned)grid), b(kBlock);
-  if (a.hd == 64) hipLaunchKernelGGL((attn_split<64, true>), g, b, 0, s, a);
-  else if (a.hd == 128) hipLaunchKernelGGL((attn_split<128, true>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((attn_split<256, true>), g, b, 0, s, a);
+  if (a.hd == 64) hipLaunchKernelGGL((attn_split<64, AFTER>), g, b, 0, s, a);
+  else if (a.hd == 128) hipLaunchKernelGGL((attn_split<128, AFTER>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((attn_split<256, AFTER>), g, b, 0, s, a);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_paged_attn_after(const PagedAttnArgs& a, hipStream_t s) {
+  return a.whole ? launch_after<After::kWhole>(a, s) : launch_after<After::kParts>(a, s);
 }
 
 namespace {
@@ -421,7 +431,7 @@ template <int HD>
 hipError_t launch_hd(const PagedAttnArgs& a, hipStream_t s) {
   const int64_t grid = own_attn_grid(a);
   if (grid > 0x7FFFFFFFLL) return hipErrorNotSupported;
-  hipLaunchKernelGGL((attn_split<HD, false>), dim3((unsigned)grid), dim3(kBlock), 0, s, a);
+  hipLaunchKernelGGL((attn_split<HD, After::kNo>), dim3((unsigned)grid), dim3(kBlock), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   return launch_attn_join(a, s);

@@ -58,7 +58,7 @@ struct PagedAttnArgs {
   const int32_t* group_starts;
   const int32_t* prefix_lens;
   int32_t groups, max_prefix;
-  int32_t prefix_splits, prefix_split_len, waves, row_tiles;   // set by plan_paged_attn_prefix
+  int32_t prefix_splits, prefix_split_len, waves, row_tiles, whole;   // set by plan_paged_attn_prefix
 };
 
 struct CacheReadArgs {
@@ -72,10 +72,14 @@ struct CacheReadArgs {
   int32_t batch, nkv, hd, block_size, num_blocks, max_blocks;
 };
 
+// What a call's workgroups of single requests are: all of it, the parts of requests behind
+// their shared prefixes, or those with the prefixes' parts taken in.
+enum class After { kNo, kParts, kWhole };
+
 // Splits of the cache's length and the workspace they need (bytes).
 int64_t plan_paged_attn(PagedAttnArgs* a);
 int64_t plan_paged_attn_fp8(PagedAttnArgs* a);
-int64_t plan_paged_attn_prefix(PagedAttnArgs* a);   // -1: more workgroups than a launch has
+int64_t plan_paged_attn_prefix(PagedAttnArgs* a, bool fp8);   // -1: more workgroups than a launch has
 // Workgroups of the requests' own tokens.
 int64_t own_attn_grid(const PagedAttnArgs& a);
 
@@ -84,6 +88,7 @@ hipError_t launch_qk_norm_fp8(const QkNormArgs& a, hipStream_t stream);
 hipError_t launch_cache_read_fp8(const CacheReadArgs& a, hipStream_t stream);
 hipError_t launch_paged_attn(const PagedAttnArgs& a, hipStream_t stream);
 hipError_t launch_paged_attn_fp8(const PagedAttnArgs& a, hipStream_t stream);
+// Requests' own tokens behind their shared prefix.
 hipError_t launch_paged_attn_after(const PagedAttnArgs& a, hipStream_t stream);
 hipError_t launch_paged_attn_after_fp8(const PagedAttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_join(const PagedAttnArgs& a, hipStream_t stream);

@@ -81,4 +81,53 @@ __device__ __forceinline__ int own_split_len(const PagedAttnArgs& a, int start, 
   return max(1, (units + a.splits - 1) / a.splits) * unit;
 }
 
+// What the attn_prefix workgroups left of rows whose own tokens a workgroup of four waves
+// has gone through: wave w takes every fourth part into its maximum m, sum l and
+// outputs O of the 16 rows from row0 on, as if it were a tile of its own. O[u VR + e] of a
+// lane is value (16 u + l16) VR + e of rows 4 lg + i; m belongs to row l16, and of l the
+// four lanes of a row have a share each.
+template <int HD, int VR, int VW>
+__device__ __forceinline__ void take_prefix(const PagedAttnArgs& a, int r, int kvh, int row0, int w,
+                                            int n_parts, float& m, float& l, f32x4* O) {
+  const int lane = (int)(threadIdx.x & 63), l16 = lane & 15, lg = lane >> 4;
+  const int group = a.nq / a.nkv, rows = group * a.nq_tok;
+  const int row_parts = a.prefix_splits + a.splits;
+  const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
+  auto first_part = [&](int row) {
+    const int j = row / group;
+    return (((int64_t)r * a.nq_tok + j) * a.nq + kvh * group + row - j * group) * row_parts;
+  };
+  const bool ok = row0 + l16 < rows;
+  const float* const ml = a.ws + first_part(ok ? row0 + l16 : 0) * 2;
+  const float* from[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + lg * 4 + i;
+    from[i] = row < rows ? a.ws + values_at(n_rows * row_parts) + first_part(row) * HD + l16 * VR : nullptr;
+  }
+  for (int p = w; p < n_parts; p += 4) {
+    f32x4 x[4][VW * VR / 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int u = 0; u < VW * VR / 4; ++u) {
+        x[i][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (from[i]) x[i][u] = *(const f32x4*)(from[i] + (int64_t)p * HD + u / (VR / 4) * 16 * VR + u % (VR / 4) * 4);
+      }
+    const float mp = ok ? ml[p * 2] : kNone, lp = ok && lg == 0 ? ml[p * 2 + 1] : 0.f;
+    const float mn = fmaxf(m, mp);
+    const float f = exp2_(m - mn), fp = exp2_(mp - mn);
+    m = mn;
+    l = l * f + lp * fp;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float fi = __shfl(f, lg * 4 + i), fpi = __shfl(fp, lg * 4 + i);
+#pragma unroll
+      for (int u = 0; u < VW * VR / 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[u * 4 + e][i] = O[u * 4 + e][i] * fi + x[i][u][e] * fpi;
+    }
+  }
+}
+
 }  // namespace sc

@@ -49,7 +49,7 @@ __device__ __forceinline__ uint32_t finite_codes(uint32_t w) {
 }  // namespace
 
 // AFTER: as in attn.hip, the call's second half behind attn_prefix.
-template <int HD, bool AFTER>
+template <int HD, After AFTER>
 __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void attn_split_fp8(PagedAttnArgs a) {
   constexpr int KC = HD / 64;               // 16-byte loads of a key row per lane
   constexpr int VPL = HD / 16;              // values of a token's row per lane
@@ -66,13 +66,13 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
   id /= (unsigned)a.batch;
   const int rg = (int)(id % (unsigned)row_groups);
   const int split = (int)(id / (unsigned)row_groups);
-  if (!AFTER && a.sorted) r = by_length(a, r);
+  if (AFTER == After::kNo && a.sorted) r = by_length(a, r);
 
   const int lane = (int)(threadIdx.x & 63);
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l16 = lane & 15, lg = lane >> 4;
   int start = 0, split_len = a.split_len;
-  if constexpr (AFTER) {
+  if constexpr (AFTER != After::kNo) {
     const int len = min(max(a.lens[r], 0), a.max_len);
     start = shared_tokens(a, r, len);
     split_len = own_split_len(a, start, len, 4 * kTurn);
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
         const int t = t0 + u * kTile + lg * 4 + i;
         // positions behind the tile's last visible one hold anything, NaN included
         const float y = times_scale(s[u][i], byte_of(cur.ks[u], i), kKeyExp) * c;
-        s[u][i] = cur.ok[u] && t <= limit && t < t_hi && (!AFTER || t >= start) ? y : -INFINITY;
+        s[u][i] = cur.ok[u] && t <= limit && t < t_hi && (AFTER == After::kNo || t >= start) ? y : -INFINITY;
         top = fmaxf(top, s[u][i]);
       }
     if (more) load_k(pg, t0 + 4 * kTurn);
@@ -220,13 +220,13 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
     // Value rows that no row of the tile sees hold anything, NaN codes included,
     // which a weight of 0 would not undo: they count as zeros. So do NaN codes that
     // only later drafts see; they are added after the loop, to those alone.
-    if (!cur.ok[0] || !cur.ok[1] || t0 + kTurn > t_hi || (AFTER && t0 < start)) {
+    if (!cur.ok[0] || !cur.ok[1] || t0 + kTurn > t_hi || (AFTER != After::kNo && t0 < start)) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = t0 + u * kTile + lg * 4 + i;
-          const bool live = cur.ok[u] && t < t_hi && (!AFTER || t >= start);
+          const bool live = cur.ok[u] && t < t_hi && (AFTER == After::kNo || t >= start);
 #pragma unroll
           for (int x = 0; x < VC; ++x) cur.v[u][i][x] = live ? cur.v[u][i][x] : 0u;
         }
@@ -291,6 +291,9 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
       }
     }
   }
+  if constexpr (AFTER == After::kWhole)
+    take_prefix<HD, VPL, 1>(a, r, kvh, rg * kRows, w,
+                       start > 0 ? (start + a.prefix_split_len - 1) / a.prefix_split_len : 0, m, l, O);
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
   // join the four waves: wave 0 takes in the others' parts. O[d] of a lane is
@@ -319,11 +322,11 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
     fx[x] = exp2_(ml[x][l16] - mt);
     lt += ll[x][l16] * fx[x];
   }
-  const bool parts = AFTER || a.splits > 1;
+  const bool parts = AFTER == After::kParts || (AFTER == After::kNo && a.splits > 1);
   const float inv = parts ? 1.f : (lt > 0.f ? 1.f / lt : 0.f);
   const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
-  const int row_parts = AFTER ? a.prefix_splits + a.splits : a.splits;
-  const int my_part = AFTER ? a.prefix_splits + split : split;
+  const int row_parts = AFTER != After::kNo ? a.prefix_splits + a.splits : a.splits;
+  const int my_part = AFTER != After::kNo ? a.prefix_splits + split : split;
   float* const wo = a.ws + values_at(n_rows * row_parts);
   const int64_t part = (q_row * a.nq + head) * row_parts + my_part;
   if (parts && row_ok && lg == 0) {
@@ -364,7 +367,7 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
 int64_t plan_paged_attn_fp8(PagedAttnArgs* a) { return plan_paged_attn(a); }
 
 namespace {
-template <bool AFTER>
+template <After AFTER>
 hipError_t launch_split(const PagedAttnArgs& a, hipStream_t s) {
   const int64_t grid = own_attn_grid(a);
   if (grid > 0x7FFFFFFFLL) return hipErrorNotSupported;
@@ -377,12 +380,12 @@ hipError_t launch_split(const PagedAttnArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_paged_attn_fp8(const PagedAttnArgs& a, hipStream_t s) {
-  const hipError_t e = launch_split<false>(a, s);
+  const hipError_t e = launch_split<After::kNo>(a, s);
   return e != hipSuccess || a.splits == 1 ? e : launch_attn_join(a, s);
 }
 
 hipError_t launch_paged_attn_after_fp8(const PagedAttnArgs& a, hipStream_t s) {
-  return launch_split<true>(a, s);
+  return a.whole ? launch_split<After::kWhole>(a, s) : launch_split<After::kParts>(a, s);
 }
 
 }  // namespace sc

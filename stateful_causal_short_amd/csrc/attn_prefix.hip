@@ -54,6 +54,7 @@ namespace {
 constexpr int kWaveRows = 32;
 constexpr int kMaxPrefixSplits = 96;
 constexpr int kMaxOwnSplits = 32;
+constexpr int kMostTakenIn = 16;   // prefix parts that workgroups of single requests take in
 // A row's maximum may pass the one that its weights refer to by 2^kSlack before the
 // outputs are rescaled: weights then reach 256, far from any limit of bf16 or fp32.
 constexpr float kSlack = 8.f;
@@ -138,7 +139,7 @@ __device__ __forceinline__ int group_of_tile(const PagedAttnArgs& a, int rows_ea
 }  // namespace
 
 template <int HD, int WAVES, bool FP8>
-__global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void attn_prefix(PagedAttnArgs a) {
+__global__ __launch_bounds__(WAVES * 64, HD == 256 ? 1 : 2) void attn_prefix(PagedAttnArgs a) {
   constexpr int TN = tile_tokens(HD, WAVES);
   constexpr int NT = WAVES * 64;
   constexpr int M = WAVES * kWaveRows;
@@ -552,12 +553,14 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 || WAVES == 1 ? 1 : 2) void a
       *(f32x4*)(wo + d * 32 + i * 8) = f32x4{O[d][i * 4], O[d][i * 4 + 1], O[d][i * 4 + 2], O[d][i * 4 + 3]};
 }
 
-// Adds a query row's parts, those of the prefix and of its own tokens. WPR waves of
-// a workgroup per row take parts in turn, hd/64 values a lane.
+// Adds a query row's parts, those of the prefix and of its own tokens, where the latter
+// are more than one or the former many. WPR waves of a workgroup per row take parts in
+// turn, hd/64 values a lane, eight loads at a time that do not wait for the weights.
 template <int HD, int WPR>
 __global__ __launch_bounds__(kBlock) void attn_prefix_join(PagedAttnArgs a, int unit) {
-  constexpr int N = HD / 64, PER = 4 / WPR;
+  constexpr int N = HD / 64, PER = 4 / WPR, AT_ONCE = 8;
   constexpr int NP = (kMaxPrefixSplits + kMaxOwnSplits) / 64;
+  typedef float row_t __attribute__((ext_vector_type(N)));
   __shared__ float part_s[4][HD];
   const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;
   const int lane = (int)(threadIdx.x & 63);
@@ -577,13 +580,24 @@ __global__ __launch_bounds__(kBlock) void attn_prefix_join(PagedAttnArgs a, int 
     const int row_parts = a.prefix_splits + a.splits;
     const float* ml = a.ws + row * row_parts * 2;
     const float* part = a.ws + values_at(n_rows * row_parts) + row * row_parts * HD + lane * N;
+    // the i-th part there is
+    auto number = [&](int i) { return i < n1 ? i : a.prefix_splits + i - n1; };
+    row_t x[AT_ONCE];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) {
+        const int i = i0 + u * WPR;
+        if (i < n1 + n2) x[u] = *(const row_t*)(part + (int64_t)number(i) * HD);
+      }
+    };
+    load(w % WPR);
     float mi[NP], f[NP], mt = kNone;
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
-      const int x = u * 64 + lane;
-      const bool in = x < n1 || (x >= a.prefix_splits && x < a.prefix_splits + n2);
-      mi[u] = in ? ml[x * 2] : kNone;
-      f[u] = in ? ml[x * 2 + 1] : 0.f;
+      const int i = u * 64 + lane;
+      const bool in = i < n1 + n2;
+      mi[u] = in ? ml[number(i) * 2] : kNone;
+      f[u] = in ? ml[number(i) * 2 + 1] : 0.f;
       mt = fmaxf(mt, mi[u]);
     }
 #pragma unroll
@@ -596,17 +610,21 @@ __global__ __launch_bounds__(kBlock) void attn_prefix_join(PagedAttnArgs a, int 
     }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) lt += __shfl_xor(lt, d);
-    // the i-th part there is
-    for (int i = w % WPR; i < n1 + n2; i += WPR) {
-      const int x = i < n1 ? i : a.prefix_splits + i - n1;
-      float fx = __shfl(f[0], x & 63);
+    for (int i0 = w % WPR; i0 < n1 + n2; i0 += AT_ONCE * WPR) {
+      if (i0 >= WPR) load(i0);
 #pragma unroll
-      for (int u = 1; u < NP; ++u) {
-        const float z = __shfl(f[u], x & 63);
-        fx = x >= u * 64 ? z : fx;
+      for (int u = 0; u < AT_ONCE; ++u) {
+        const int i = i0 + u * WPR;
+        if (i >= n1 + n2) break;
+        float fi = __shfl(f[0], i & 63);
+#pragma unroll
+        for (int v = 1; v < NP; ++v) {
+          const float z = __shfl(f[v], i & 63);
+          fi = i >= v * 64 ? z : fi;
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) y[e] = fmaf(x[u][e], fi, y[e]);
       }
-#pragma unroll
-      for (int e = 0; e < N; ++e) y[e] = fmaf(part[(int64_t)x * HD + e], fx, y[e]);
     }
   }
   if constexpr (WPR > 1) {
@@ -625,32 +643,72 @@ __global__ __launch_bounds__(kBlock) void attn_prefix_join(PagedAttnArgs a, int 
   for (int e = 0; e < N; ++e) o[e] = (uint16_t)pack_bf16(y[e] * inv, 0.f);
 }
 
-int64_t plan_paged_attn_prefix(PagedAttnArgs* a) {
+namespace {
+
+// About how long attn_prefix and the way of its parts take (us) with `splits` of the
+// prefix and `waves` in a workgroup. Measured, 64 tokens x 128: a tile takes 0.9 us (0.6
+// with 32 tokens) and 0.17 for each busy wave on its CU, widening codes 0.17 for each
+// workgroup of fewer than eight waves there; a call 7 us to begin and end, a part 1 us for
+// each 2 MB there and back, a join launch 4; the prefix comes at 5.5 TB/s. So for 256 rows x
+// 4 heads on 16,384 tokens 4 waves and 32 splits are taken, 38 us (8 and 32: 42, 4 and
+// 16: 41); for 1,024 rows on 4,096 4 and 8, 41 us (8 and 16: 43, 4 and 16: 43); for 2,048 on
+// 32,768 8 and 8, 220 us (4 and 4: 276); for 10 groups of 201 requests x 8 rows x 64 on up
+// to 8,192 2 and 8, 50 us (4 and 5: 55, 8 and 4: 61).
+struct PrefixTime {
+  PrefixTime(const PagedAttnArgs& a, int waves, int64_t rows, int64_t groups, bool fp8) {
+    cus = device_cus();
+    tn = tile_tokens(a.hd, waves);
+    units = (a.max_prefix + tn - 1) / tn;
+    const int64_t tiles = (rows - groups) / (waves * kWaveRows) + groups;
+    each = tiles * a.nkv;
+    slots = (a.hd == 256 ? 4 : 8) / waves * cus;
+    base_us = tn == 64 || a.hd == 256 ? 0.9 : 0.6;
+    // a workgroup's, of its busy waves
+    more_us = 0.17 * tn * a.hd / 8192 * ((double)rows / kWaveRows + groups * 0.5) / tiles +
+              (fp8 && waves < 8 ? 0.17 : 0);
+    read_us = (double)groups * a.max_prefix * a.nkv * a.hd * (fp8 ? 2 : 4) / 5.5e6;
+    part_us = (double)rows * a.nkv * a.hd * 4 / 2.2e6;
+    uneven = groups > 1;
+  }
+  double of(int64_t splits) const {
+    const int64_t total = each * splits;
+    const int64_t at_once = std::min((total + cus - 1) / cus, slots / cus);
+    // groups have prefixes of several lengths, so that rounds of their workgroups run together
+    const double rounds = uneven ? std::max(1.0, (double)total / slots) : (double)((total + slots - 1) / slots);
+    const int64_t turns = (units + splits - 1) / splits;
+    return std::max(rounds * turns * (base_us + more_us * at_once), read_us) + splits * part_us + 7 +
+           (splits > kMostTakenIn ? 4 : 0);
+  }
+  double base_us, more_us, read_us, part_us;
+  int64_t cus, each, slots, tn, units;     // each: workgroups of a split
+  bool uneven;
+};
+
+}  // namespace
+
+int64_t plan_paged_attn_prefix(PagedAttnArgs* a, bool fp8) {
   const int64_t rows_each = (int64_t)(a->nq / a->nkv) * a->nq_tok;
   const int64_t rows = a->batch * rows_each;
   const int64_t groups = std::max<int64_t>(1, std::min(a->groups, a->batch));
   const int64_t cus = device_cus();
-  // as many waves as an average group has rows for; 256-wide heads leave registers for
-  // four, and a tile of them is too much for one wave to move
-  const int most = a->hd == 256 ? 4 : 8;
-  a->waves = a->hd == 256 ? 2 : 1;
-  while (a->waves < most && (int64_t)a->waves * kWaveRows * groups < rows) a->waves *= 2;
+  // 256-wide heads leave registers for four waves
+  int64_t best = 1;
+  double best_us = -1;
+  for (int waves = a->hd == 256 ? 4 : 8; waves >= 2; waves /= 2) {
+    const PrefixTime time(*a, waves, rows, groups, fp8);
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(time.units, kMaxPrefixSplits));
+    auto look = [&](int64_t n) {
+      n = std::clamp<int64_t>(n, 1, most);
+      const double us = time.of(n);
+      if (best_us < 0 || us < best_us) a->waves = waves, best = n, best_us = us;
+    };
+    for (int64_t n : {1, 2, 4, 8, 16, 32, 64, 96}) look(n);
+    look(time.cus / time.each);                         // as fill the chip once
+    look(time.slots / time.each);
+  }
   const int64_t m = (int64_t)a->waves * kWaveRows, tn = tile_tokens(a->hd, a->waves);
   const int64_t tiles = (rows - groups) / m + groups;   // the groups' last tiles may be part
-  const int64_t each = tiles * a->nkv;                  // workgroups of a split
   const int64_t units = (a->max_prefix + tn - 1) / tn;
-  // Splits of the prefix: those for which rounds of workgroups on the chip, each as long as
-  // its tiles and about 4 us of start and end, and the join's traffic come out shortest.
-  const int64_t per_cu = a->waves == 8 ? 1 : a->waves == 4 ? 2 : 4;
-  const double tile_us = per_cu * std::max(m * tn * a->hd * 4 / 3.0e6, tn * a->hd * 4 / 2.0e4);
-  const double part_us = (double)rows * a->nkv * a->hd * 8 / 4.0e6;
-  int64_t best = 1;
-  double best_us = 0;
-  for (int64_t s = 1; s <= std::min<int64_t>(units, kMaxPrefixSplits); ++s) {
-    const int64_t rounds = (each * s + per_cu * cus - 1) / (per_cu * cus);
-    const double us = rounds * ((units + s - 1) / s * tile_us + 4) + s * part_us;
-    if (s == 1 || us < best_us) best = s, best_us = us;
-  }
   const int64_t per = std::max<int64_t>(1, (units + best - 1) / best);
   a->prefix_splits = (int32_t)((units + per - 1) / per);
   a->prefix_split_len = (int32_t)(per * tn);
@@ -661,7 +719,9 @@ int64_t plan_paged_attn_prefix(PagedAttnArgs* a) {
   const int64_t left = a->max_len - a->max_prefix + kTile;
   const int64_t want = base >= 4 * cus ? 8 * cus : 16 * cus;
   a->splits = (int32_t)std::max<int64_t>(
-      1, std::min<int64_t>({(want + base - 1) / base, (left + 511) / 512, kMaxOwnSplits}));
+      1, std::min<int64_t>({(want + base - 1) / base, (left + 1023) / 1024, kMaxOwnSplits}));
+  // One split of them takes the prefix's parts in by itself, a wave a fourth of them.
+  a->whole = a->splits == 1 && a->prefix_splits <= kMostTakenIn;
   a->sorted = 0;
   if (tiles * a->nkv * std::max(a->prefix_splits, 1) > 0x7FFFFFF0LL) return -1;
   const int64_t parts = (int64_t)a->batch * a->nq_tok * a->nq * (a->prefix_splits + a->splits);
@@ -681,15 +741,12 @@ hipError_t launch_hd(const PagedAttnArgs& a, hipStream_t s) {
   if (a.prefix_splits > 0) {
     if (a.waves == 2) launch_prefix<HD, 2, FP8>(a, s);
     else if (a.waves == 4) launch_prefix<HD, 4, FP8>(a, s);
-    else if constexpr (HD != 256) {
-      if (a.waves == 1) launch_prefix<HD, 1, FP8>(a, s);
-      else launch_prefix<HD, 8, FP8>(a, s);
-    }
+    else if constexpr (HD != 256) launch_prefix<HD, 8, FP8>(a, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const hipError_t e = FP8 ? launch_paged_attn_after_fp8(a, s) : launch_paged_attn_after(a, s);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || a.whole) return e;
   // a workgroup per row until rows alone fill the chip
   const int64_t rows = (int64_t)a.batch * a.nq_tok * a.nq;
   const int unit = FP8 ? 128 : 64;
