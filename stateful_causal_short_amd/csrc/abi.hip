@@ -340,6 +340,11 @@ sc_status attn_bounds(const sc_paged_attn_desc* d, int32_t max_blocks, int32_t m
              : SC_OK;
 }
 
+// Whether a lane's offset in 16 tokens has 31 bits.
+bool tokens_near(const sc::PagedAttnArgs& a) {
+  return std::max({a.kc.token_s, a.vc.token_s, a.kc8.token_s, a.vc8.token_s}) < (1 << 26);
+}
+
 template <class Cache>
 sc_status attn_prefix_call(const sc_paged_attn_desc* desc, const void* q, void* out,
                            const Cache* k_cache, const Cache* v_cache, const int32_t* block_table,
@@ -361,9 +366,7 @@ sc_status attn_prefix_call(const sc_paged_attn_desc* desc, const void* q, void* 
   st = attn_args(desc, q, out, k_cache, v_cache, block_table, seq_lens, max_seq_len, workspace,
                  workspace_bytes, need, &a);
   if (st != SC_OK) return st;
-  // a lane's offset in 16 tokens has 32 bits
-  if (std::max({a.kc.token_s, a.vc.token_s, a.kc8.token_s, a.vc8.token_s}) >= (1 << 26))
-    return SC_ERR_UNSUPPORTED;
+  if (!tokens_near(a)) return SC_ERR_UNSUPPORTED;
   a.group_starts = group_start_loc;
   a.prefix_lens = prefix_lens;
   return from_hip(sc::launch_paged_attn_prefix(a, fp8, (hipStream_t)stream));
@@ -985,6 +988,7 @@ sc_status sc_paged_attn_decode_fp8(const sc_paged_attn_desc* desc, const void* q
   st = attn_args(desc, q, out, k_cache, v_cache, block_table, seq_lens, max_seq_len, workspace,
                  workspace_bytes, need, &a);
   if (st != SC_OK) return st;
+  if (!tokens_near(a)) return SC_ERR_UNSUPPORTED;
   return from_hip(sc::launch_paged_attn_fp8(a, (hipStream_t)stream));
 }
 

@@ -59,6 +59,13 @@ __device__ __forceinline__ int by_length(const PagedAttnArgs& a, int i) {
 // aligned, its hd values. The float at which those begin, for n of them:
 __host__ __device__ inline int64_t values_at(int64_t n) { return (n * 2 + 3) & ~(int64_t)3; }
 
+// Lane n's value, for all lanes.
+__device__ __forceinline__ int64_t lane_of(int64_t x, int n) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, n);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), n);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Leading tokens of request r that attn_prefix takes for its whole group: those of
 // the group, if each of its new tokens sees all of them; else none.
 __device__ __forceinline__ int shared_tokens(const PagedAttnArgs& a, int r, int len) {

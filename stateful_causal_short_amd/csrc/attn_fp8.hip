@@ -35,6 +35,12 @@ constexpr float kKeyUnit = 1.f / (1 << kKeyExp);
 template <int N>
 using CodeRun = uint32_t __attribute__((ext_vector_type(N / 4)));
 
+// The scale in byte i of a word, as a factor (2^-127 has no exponent of its own).
+__device__ __forceinline__ float scale_of(uint32_t w, int i) {
+  const uint32_t x = (i == 3 ? w >> 1 : w << (23 - 8 * i)) & 0x7F800000u;
+  return __uint_as_float(x > 0x00400000u ? x : 0x00400000u);
+}
+
 __device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xFFu; }
 
 // NaN codes (0x7F and 0xFF) of a word replaced by zeros.
@@ -78,19 +84,34 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
     split_len = own_split_len(a, start, len, 4 * kTurn);
   }
   const int t_lo = (start & ~(kTile - 1)) + split * split_len;
-  // page ids run a turn ahead of the loads that need them
+  // The wave's n-th tile is at t_mine(n). Its place in the caches is kept in lane n, for 64
+  // tiles at a time, so that a tile costs a few lane reads, and its page's id is there
+  // long before. A tile lies in one page; below max_len it has an entry in the table.
   const int32_t* const table = a.table + (int64_t)r * a.table_rs;
-  auto page_of = [&](int t) { return t < a.max_len ? table[t / a.block_size] : -1; };
-  int t0 = t_lo + w * kTurn;
-  int page[2], page_next[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    page[u] = page_of(t0 + u * kTile);
-    page_next[u] = page_of(t0 + 4 * kTurn + u * kTile);
-  }
+  auto t_mine = [&](int n) { return (uint32_t)(t_lo + w * kTurn) + (n >> 1) * 4 * kTurn + (n & 1) * kTile; };
+  auto page_of = [&](int n) {
+    const uint32_t t = t_mine(n + lane);
+    return t < (uint32_t)a.max_len ? table[t / a.block_size] : -1;
+  };
+  auto in_cache = [&](int pg) { return pg >= 0 && pg < a.num_blocks; };
+  struct Places {
+    int64_t k, v, ks, vs;
+    uint64_t ok;           // a page id outside the cache makes the tile invisible
+  };
+  auto places = [&](int n, int page) {
+    const int in = t_mine(n + lane) % a.block_size;
+    const int64_t b = in_cache(page) ? page : 0;
+    return Places{kvh * a.kc8.head_s + b * a.kc8.block_s + in * a.kc8.token_s,
+                  kvh * a.vc8.head_s + b * a.vc8.block_s + in * a.vc8.token_s,
+                  kvh * a.kc8.scale_head_s + b * a.kc8.scale_block_s + in,
+                  kvh * a.vc8.scale_head_s + b * a.vc8.scale_block_s + in, __ballot(in_cache(page))};
+  };
+  int page = page_of(0);
   const int len = min(max(a.lens[r], 0), a.max_len);
   const int t_hi = min(len, t_lo + split_len);
   if (split > 0 && t_lo >= len) return;      // the join does not read such a split
+  int t0 = t_lo + w * kTurn;
+  const int n_tiles = t0 < t_hi ? (t_hi - t0 + 4 * kTurn - 1) / (4 * kTurn) * 2 : 0;
 
   // this lane's query row: head kvh * group + g of new token j
   const int row = rg * kRows + l16;
@@ -115,56 +136,52 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
   f32x4 O[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) O[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const float c = a.scale * 1.4426950408889634f;
-  const uint8_t* const kbase = (const uint8_t*)a.kc8.p + (int64_t)kvh * a.kc8.head_s;
-  const uint8_t* const vbase = (const uint8_t*)a.vc8.p + (int64_t)kvh * a.vc8.head_s;
-  const uint8_t* const ksbase = a.kc8.scale + (int64_t)kvh * a.kc8.scale_head_s + lg * 4;
-  const uint8_t* const vsbase = a.vc8.scale + (int64_t)kvh * a.vc8.scale_head_s + lg * 4;
+  const float c = a.scale * 1.4426950408889634f * (1 << kKeyExp);
+  // a lane's own offsets in a tile (token strides are checked to leave 32 bits)
+  const uint32_t k_lane = (uint32_t)l16 * (uint32_t)a.kc8.token_s + lg * 16;
+  uint32_t v_lane[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v_lane[i] = (uint32_t)(lg * 4 + i) * (uint32_t)a.vc8.token_s + l16 * VPL;
 
   struct {
     u32x4 k[2][KC];
     CodeRun<VPL> v[2][4];
     uint32_t ks[2], vs[2];
-    bool ok[2];
   } cur;
-  auto in_cache = [&](int pg) { return pg >= 0 && pg < a.num_blocks; };
-  // A tile lies in one page. A page id outside the cache makes the tile invisible.
-  auto load_k = [&](const int* pg, int t) {
+  auto load_k = [&](const Places& x, int n) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t b = in_cache(pg[u]) ? pg[u] : 0;
-      const int in = (t + u * kTile) % a.block_size;
-      const uint8_t* kp = kbase + b * a.kc8.block_s + (int64_t)(in + l16) * a.kc8.token_s + lg * 16;
+      const uint8_t* kp = (const uint8_t*)a.kc8.p + lane_of(x.k, n + u);
 #pragma unroll
-      for (int s = 0; s < KC; ++s) cur.k[u][s] = ld16(kp + s * 64);
-      cur.ks[u] = *(const uint32_t*)(ksbase + b * a.kc8.scale_block_s + in);
+      for (int s = 0; s < KC; ++s) cur.k[u][s] = ld16(kp + k_lane + s * 64);
+      cur.ks[u] = *(const uint32_t*)(a.kc8.scale + lane_of(x.ks, n + u) + lg * 4u);
     }
   };
-  auto load_v = [&](const int* pg, int t) {
+  auto load_v = [&](const Places& x, int n) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t b = in_cache(pg[u]) ? pg[u] : 0;
-      const int in = (t + u * kTile) % a.block_size;
-      const uint8_t* vp = vbase + b * a.vc8.block_s + (int64_t)(in + lg * 4) * a.vc8.token_s + l16 * VPL;
+      const uint8_t* vp = (const uint8_t*)a.vc8.p + lane_of(x.v, n + u);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) cur.v[u][i] = *(const CodeRun<VPL>*)(vp + (int64_t)i * a.vc8.token_s);
-      cur.vs[u] = *(const uint32_t*)(vsbase + b * a.vc8.scale_block_s + in);
+      for (int i = 0; i < 4; ++i) cur.v[u][i] = *(const CodeRun<VPL>*)(vp + v_lane[i]);
+      cur.vs[u] = *(const uint32_t*)(a.vc8.scale + lane_of(x.vs, n + u) + lg * 4u);
     }
   };
-  if (t0 < t_hi) {
-    load_k(page, t0);
-    load_v(page, t0);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) cur.ok[u] = in_cache(page[u]);
+  Places at = places(0, page);
+  if (n_tiles > 64) page = page_of(64);
+  uint32_t ok = 0;
+  if (n_tiles > 0) {
+    load_k(at, 0);
+    load_v(at, 0);
+    ok = (uint32_t)at.ok & 3;
   }
-  for (; t0 < t_hi; t0 += 4 * kTurn) {
-    const bool more = t0 + 4 * kTurn < t_hi;
-    int pg[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      pg[u] = page_next[u];
-      page_next[u] = page_of(t0 + 8 * kTurn + u * kTile);
+  for (int n = 0; n < n_tiles; n += 2, t0 += 4 * kTurn) {
+    const bool more = n + 2 < n_tiles;
+    if (more && (n + 2) % 64 == 0) {
+      at = places(n + 2, page);
+      if (n_tiles > n + 66) page = page_of(n + 66);
     }
+    // every row sees every token of the turn
+    const bool plain = ok == 3 && t0 + kTurn <= min(first_new, t_hi) && (AFTER == After::kNo || t0 >= start);
     f32x4 s[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -179,14 +196,25 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = t0 + u * kTile + lg * 4 + i;
-        // positions behind the tile's last visible one hold anything, NaN included
-        const float y = times_scale(s[u][i], byte_of(cur.ks[u], i), kKeyExp) * c;
-        s[u][i] = cur.ok[u] && t <= limit && t < t_hi && (AFTER == After::kNo || t >= start) ? y : -INFINITY;
-        top = fmaxf(top, s[u][i]);
-      }
-    if (more) load_k(pg, t0 + 4 * kTurn);
+      for (int i = 0; i < 4; ++i) s[u][i] = s[u][i] * scale_of(cur.ks[u], i) * c;
+    if (!plain) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = t0 + u * kTile + lg * 4 + i;
+          // positions behind the tile's last visible one hold anything, NaN included
+          if (!(ok >> u & 1) || t > limit || t >= t_hi || (AFTER != After::kNo && t < start)) {
+            s[u][i] = -INFINITY;
+            cur.vs[u] &= ~(0xFFu << i * 8);
+          }
+        }
+    }
+    if (more) load_k(at, (n + 2) & 63);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[u][i]);
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     // the accumulators are rescaled only when some row's maximum grows
@@ -211,7 +239,7 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
         const float p0 = exp2_(s[u][i] - m), p1 = exp2_(s[u][i + 1] - m);
         l += p0;
         l += p1;
-        f32x2 y = {times_scale(p0, byte_of(cur.vs[u], i)), times_scale(p1, byte_of(cur.vs[u], i + 1))};
+        f32x2 y = {p0 * scale_of(cur.vs[u], i), p1 * scale_of(cur.vs[u], i + 1)};
         const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2));
         f32x2 z = {y[0] - __uint_as_float(h << 16), y[1] - __uint_as_float(h & 0xFFFF0000u)};
         hi[u * 2 + i / 2] = h;
@@ -220,13 +248,13 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
     // Value rows that no row of the tile sees hold anything, NaN codes included,
     // which a weight of 0 would not undo: they count as zeros. So do NaN codes that
     // only later drafts see; they are added after the loop, to those alone.
-    if (!cur.ok[0] || !cur.ok[1] || t0 + kTurn > t_hi || (AFTER != After::kNo && t0 < start)) {
+    if (!plain) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = t0 + u * kTile + lg * 4 + i;
-          const bool live = cur.ok[u] && t < t_hi && (AFTER == After::kNo || t >= start);
+          const bool live = (ok >> u & 1) && t < t_hi && (AFTER == After::kNo || t >= start);
 #pragma unroll
           for (int x = 0; x < VC; ++x) cur.v[u][i][x] = live ? cur.v[u][i][x] : 0u;
         }
@@ -267,9 +295,10 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
                                                     __builtin_bit_cast(bf16x8, v), o, 0, 0, 0);
       }
     }
-    if (more) load_v(pg, t0 + 4 * kTurn);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) cur.ok[u] = in_cache(pg[u]);
+    if (more) {
+      load_v(at, (n + 2) & 63);
+      ok = (uint32_t)(at.ok >> ((n + 2) & 63)) & 3;
+    }
   }
   if (__any(odd)) {
 #pragma unroll 1
@@ -277,7 +306,8 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
       if ((((t - t_lo) / kTurn) & 3) != w) continue;
       const int b = t / a.block_size, pg = table[b];
       if (!in_cache(pg)) continue;
-      const uint8_t* vp = vbase + pg * a.vc8.block_s + (int64_t)(t - b * a.block_size) * a.vc8.token_s + l16 * VPL;
+      const uint8_t* vp = (const uint8_t*)a.vc8.p + kvh * a.vc8.head_s + pg * a.vc8.block_s +
+                          (int64_t)(t - b * a.block_size) * a.vc8.token_s + l16 * VPL;
       bool sees[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) sees[i] = __shfl(limit, lg * 4 + i) >= t;
@@ -364,7 +394,38 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
   }
 }
 
-int64_t plan_paged_attn_fp8(PagedAttnArgs* a) { return plan_paged_attn(a); }
+int64_t plan_paged_attn_fp8(PagedAttnArgs* a) {
+  const int64_t rows = (int64_t)(a->nq / a->nkv) * a->nq_tok;
+  const int64_t base = (int64_t)a->batch * a->nkv * ((rows + kRows - 1) / kRows);
+  const int64_t unit = 4 * kTurn;            // tokens of one turn of the four waves
+  const int64_t units = std::max<int64_t>(1, (a->max_len + unit - 1) / unit);
+  // Two workgroups a CU stream as fast as three (all that its registers hold), so the
+  // split makes two, of 256 tokens or more. Where the requests alone give one a CU,
+  // it only evens out unequal lengths, up to four a CU, if 2,048 tokens or more are left
+  // to each. 16 query and 4 key/value heads x 128, us with 1, 2, 4, .. 64 splits:
+  //   1 x 2,048              22 17 13 11 10 10 10
+  //   1 x 8,192              78 43 26 18 14 13 13
+  //   4 x 4,096              43 28 19 14 13 14 14
+  //   4 of up to 32,768     262 140 75 43 28 26 31
+  //   16 of up to 8,192      77 46 29 25 26 29 37
+  //   16 x 32,768           368 200 126 120 125 125 132
+  //   64 of up to 8,192     105 81 75 74 77 91 129
+  //   64 x 2,000             33 35 36 39 46 46 46
+  //   256 of up to 2,048     67 77 83 99 135 134 134
+  const int64_t cus = device_cus();
+  int64_t splits = base < cus ? std::min((2 * cus + base - 1) / base, units / 2)
+                              : std::min(4 * cus / base, units / (2048 / unit));
+  splits = std::clamp<int64_t>(splits, 1, kMaxSplits);
+  const int64_t per = (units + splits - 1) / splits;
+  splits = (units + per - 1) / per;
+  a->splits = (int32_t)splits;
+  a->split_len = (int32_t)(per * unit);
+  // the longest first, as in plan_paged_attn, where some workgroups wait for a CU
+  a->sorted = base * splits > 3 * cus && a->batch > 1 && a->batch <= kSortMax && a->max_len >= 512;
+  if (splits == 1) return 0;
+  const int64_t parts = (int64_t)a->batch * a->nq_tok * a->nq * splits;
+  return (values_at(parts) + parts * a->hd) * (int64_t)sizeof(float);
+}
 
 namespace {
 template <After AFTER>

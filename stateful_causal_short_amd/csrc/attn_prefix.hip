@@ -232,11 +232,6 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 ? 1 : 2) void attn_prefix(Pag
     x.ok = __ballot(ok);
     return x;
   };
-  auto lane_of = [&](int64_t x, int n) SC_INLINE {
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, n);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), n);
-    return (int64_t)((uint64_t)hi << 32 | lo);
-  };
   // Chunk i of a thread: the piece it is in, and its row's first in the piece.
   auto piece = [&](int n, int i) SC_INLINE { return n + (RP >= kTile ? i * (RP / kTile) + w_piece : i * RP / kTile); };
   constexpr auto row_in = [](int i) { return RP >= kTile ? 0 : (i * RP) & (kTile - 1); };

@@ -13,9 +13,9 @@
 
 namespace sc {
 
-// x 2^(byte - 127 + more), exact in fp32's range whatever the byte.
-__device__ __forceinline__ float times_scale(float x, uint32_t byte, int more = 0) {
-  return __builtin_amdgcn_ldexpf(x, (int)byte - 127 + more);
+// x 2^(byte - 127), exact in fp32's range whatever the byte.
+__device__ __forceinline__ float times_scale(float x, uint32_t byte) {
+  return __builtin_amdgcn_ldexpf(x, (int)byte - 127);
 }
 
 // Two codes of a word as bf16 values, times a power of two.
