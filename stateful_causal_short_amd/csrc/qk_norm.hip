@@ -8,12 +8,15 @@
 // half-split rotation a lane owns values 4l.. and rot/2 + 4l.., so both members
 // of a pair are in one lane and nothing is exchanged after the norm's sum. The
 // same lanes take several heads of a token in turn, with the token's cos and
-// sin in registers. All arithmetic is fp32 with one rounding at the store. The
+// sin in registers. All arithmetic is fp32 with one rounding at the store; what goes
+// to a quantised cache is rounded to its code from fp64. The
 // kernel moves bytes: each row is read once and written once (keys twice with
 // k_out and a cache). 32,768 tokens of 16 + 2 + 2 heads x 128, 355 MB: 84 us
 // (4.2 TB/s; a row copy reaches 5.8). Loading the next heads while these are
 // stored took 90 us, two heads at a time 87, ten 84. 17 tokens: 3.5 us, the
-// latency of three dependent loads.
+// latency of three dependent loads. Into a quantised cache, 16 + 4 + 4 heads: 32,768
+// tokens, 373 MB, 82-87 us; 85 with fp32 keys. Two to sixteen times as many workgroups
+// of fewer heads took 85 to 122 us, streaming loads and stores 88. 17 tokens: 4.1 us.
 #include "attn.hpp"
 #include "common.hpp"
 #include "fp8_device.hpp"
@@ -37,11 +40,60 @@ __device__ __forceinline__ uint2 pack4(const float* f) {
 }
 
 // Sum over the L lanes of a head (8, 16 or 32, aligned).
-template <int L>
-__device__ __forceinline__ float head_sum(float x) {
+template <int L, typename T>
+__device__ __forceinline__ T head_sum(T x) {
 #pragma unroll
   for (int d = L / 2; d >= 1; d >>= 1) x += __shfl_xor(x, d);
   return x;
+}
+
+// A lane's values of a query or key head, normalised and turned: `wp` the weights or
+// NULL, half-split pairs (e, 4 + e) or neighbours.
+template <int HD, typename T>
+__device__ __forceinline__ void norm_turn(T* x, float eps, const uint16_t* wp, int d0, int d1, bool turns,
+                                          bool interleaved, const float* cs, const float* sn) {
+  T ss = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) ss = fma(x[e], x[e], ss);
+  ss = head_sum<HD / 8>(ss) * (T)(1.f / HD) + eps;
+  T inv;
+  if constexpr (sizeof(T) == 4) inv = rsqrtf(ss);
+  else inv = rsqrt(ss);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= inv;
+  if (wp) {
+    float wv[8];
+    unpack4(*(const uint2*)(wp + d0), wv);
+    unpack4(*(const uint2*)(wp + d1), wv + 4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= wv[e];
+  }
+  if (!turns) return;
+  if (interleaved) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const T y1 = x[2 * e], y2 = x[2 * e + 1];
+      x[2 * e] = y1 * cs[e] - y2 * sn[e];
+      x[2 * e + 1] = y2 * cs[e] + y1 * sn[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const T y1 = x[e], y2 = x[4 + e];
+      x[e] = y1 * cs[e] - y2 * sn[e];
+      x[4 + e] = y2 * cs[e] + y1 * sn[e];
+    }
+  }
+}
+
+// y in fp32, cut and its last bit set if that lost something: rounding it to fewer
+// bits then gives what rounding y itself would.
+__device__ __forceinline__ float to_odd(double y) {
+  const float f = (float)y;
+  uint32_t u = __float_as_uint(f);
+  if (!(fabsf(f) < INFINITY) || (double)f == y) return f;
+  u -= fabs((double)f) > fabs(y);
+  return __uint_as_float(u | 1u);
 }
 
 // Largest finite magnitude of a head (its bits), over its lanes.
@@ -58,8 +110,7 @@ __device__ __forceinline__ uint32_t head_top(const float* x) {
   return top;
 }
 
-// A lane's two runs of four values of a head, quantised to their cache row: keys
-// straight from fp32, one rounding. `row` is the head's place, d0 and d1 the runs'.
+// A lane's two runs of four values of a head, at d0 and d1, quantised to their cache row.
 template <int L>
 __device__ __forceinline__ void store_fp8(const float* x, const PagedCacheFp8& c, int64_t block,
                                           int64_t in_block, int h, int d0, int d1, bool first) {
@@ -160,47 +211,30 @@ __global__ __launch_bounds__(kBlock) void qk_norm_rope(QkNormArgs a, int per) {
       float x[8];
       unpack4(x0[n], x);
       unpack4(x1[n], x + 4);
-      float ss = 0.f;
+      const uint16_t* const wp = (const uint16_t*)(is_q ? a.q_w : a.k_w);
+      // A key's codes are rounded once, from 64-bit values. fp32 ones lie on the other
+      // side of a tie about once in a million, a step of 2^-3 for an error of 2^-23.
+      if constexpr (FP8) {
+        if (!is_q && block >= 0) {
+          double y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-      const float inv = rsqrtf(head_sum<L>(ss) * (1.f / HD) + a.eps);
+          for (int e = 0; e < 8; ++e) y[e] = x[e];
+          norm_turn<HD>(y, a.eps, wp, d0, d1, turns, a.interleaved, cs, sn);
+          float z[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= inv;
-      if (const uint16_t* wp = (const uint16_t*)(is_q ? a.q_w : a.k_w)) {
-        float wv[8];
-        unpack4(*(const uint2*)(wp + d0), wv);
-        unpack4(*(const uint2*)(wp + d1), wv + 4);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= wv[e];
-      }
-      if (turns) {
-        if (a.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y1 = x[2 * e], y2 = x[2 * e + 1];
-            x[2 * e] = y1 * cs[e] - y2 * sn[e];
-            x[2 * e + 1] = y2 * cs[e] + y1 * sn[e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y1 = x[e], y2 = x[4 + e];
-            x[e] = y1 * cs[e] - y2 * sn[e];
-            x[4 + e] = y2 * cs[e] + y1 * sn[e];
-          }
+          for (int e = 0; e < 8; ++e) z[e] = to_odd(y[e]);
+          store_fp8<L>(z, a.kc8, block, in_block, h - a.nq, d0, d1, l == 0);
         }
+        if (!is_q && !a.k_out) continue;
       }
+      norm_turn<HD>(x, a.eps, wp, d0, d1, turns, a.interleaved, cs, sn);
       const uint2 y0 = pack4(x), y1 = pack4(x + 4);
       if (is_q || a.k_out) {
         uint16_t* d = is_q ? qo + (int64_t)h * HD : ko + (int64_t)(h - a.nq) * HD;
         *(uint2*)(d + d0) = y0;
         *(uint2*)(d + d1) = y1;
       }
-      if (!is_q && block >= 0) {
-        if constexpr (FP8) {
-          store_fp8<L>(x, a.kc8, block, in_block, h - a.nq, d0, d1, l == 0);
-          continue;
-        }
+      if (!FP8 && !is_q && block >= 0) {
         uint16_t* d = kc + (int64_t)(h - a.nq) * a.kc.head_s;
         *(uint2*)(d + d0) = y0;
         *(uint2*)(d + d1) = y1;

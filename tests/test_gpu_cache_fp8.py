@@ -92,6 +92,29 @@ def test_quantising_write(case):
         assert bool((s.transpose(1, 2)[~written] == 77).all())
 
 
+@pytest.mark.parametrize("hd, rot, inter", [(128, 128, False), (64, 32, True), (256, 0, False)])
+def test_key_codes_are_the_nearest(hd, rot, inter):
+    """Every key code and byte is that of the norm in 64 bits. Both sides are off by
+    some 2^-50 of a value and eps by 2^-24 of its own 2^-17 part of the sum; of two
+    million values spread over steps of 2^-4 one in some 10^4 runs could differ."""
+    T, nkv, block = 1 << 20 >> (hd.bit_length() - 1), 2, 16
+    print(f"[gpu] key codes {hd} {rot} {inter}", flush=True)
+    g = torch.Generator().manual_seed(hd)
+    k, w = randn(g, T, nkv * hd), randn(g, hd)
+    ang = torch.arange(T, dtype=F64)[:, None] * torch.rand(max(rot // 2, 1), generator=g, dtype=F64)
+    table = torch.cat([ang.cos(), ang.sin()], 1).float() if rot else None
+    pos = np.arange(T)
+    c = caches_fp8("heads", T // block, block, nkv, hd)
+    d = k.cuda()
+    scs().sc_qk_norm_rope_fp8(d, d, d, torch.empty_like(d), None, None, w.cuda(),
+                              None if table is None else table.cuda(),
+                              i64(pos) if rot else None, i64(pos), *c,
+                              head_dim=hd, eps=1e-5, interleaved=inter)
+    codes, byte = quantise(norm_ref(k, w, table, pos, hd, 1e-5, inter))
+    assert torch.equal(c[0].view(U8).cpu().reshape(T, nkv, hd), codes)
+    assert torch.equal(c[1].view(U8).cpu().transpose(1, 2).reshape(T, nkv), byte)
+
+
 def test_values_at_the_ends_of_the_format():
     """Heads of zeros, of one size, at 448 and the next bf16 above it, ties, the
     smallest and largest bf16 values, infinities and NaN: each value the format's."""
