@@ -34,8 +34,15 @@ __device__ __forceinline__ u32x4 fp8_to_bf16(uint32_t w0, uint32_t w1, float by 
 // A scale as the float whose exponent the conversions take.
 __device__ __forceinline__ float scale_float(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Sixteen codes times their scale, through fp32.
+// Sixteen codes times their scale: by the conversion itself where no product leaves
+// the normal range, else through fp32.
 __device__ __forceinline__ void fp8_to_bf16_scaled(u32x4 w, uint32_t byte, u32x4* y) {
+  if (byte - 16u < 224u) {
+    const float by = scale_float(byte);
+    y[0] = fp8_to_bf16(w[0], w[1], by);
+    y[1] = fp8_to_bf16(w[2], w[3], by);
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
