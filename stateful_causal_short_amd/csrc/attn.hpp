@@ -35,18 +35,17 @@ struct QkNormArgs {
   const int64_t* positions;
   const int64_t* slots;      // nullable without caches
   PagedCache kc, vc;         // p nullable: no write
-  PagedCacheFp8 kc8, vc8;    // quantised caches in their place
   int64_t q_rs, k_rs, v_rs, qo_rs, ko_rs, table_rs, max_pos;
   int64_t num_tokens;
   float eps;
   int32_t nq, nkv, hd, rot, interleaved, table_f32, block_size, num_blocks;
+  PagedCacheFp8 kc8, vc8;    // quantised caches in place of kc and vc; last, bf16 calls do not fetch them
 };
 
 struct PagedAttnArgs {
   const void* q;
   void* out;
   PagedCache kc, vc;
-  PagedCacheFp8 kc8, vc8;    // quantised caches in their place
   const int32_t* table;      // (batch, max_blocks) at table_rs
   const int32_t* lens;
   float* ws;                 // partial results when split, else nullptr
@@ -59,6 +58,7 @@ struct PagedAttnArgs {
   const int32_t* prefix_lens;
   int32_t groups, max_prefix;
   int32_t prefix_splits, prefix_split_len, waves, row_tiles, whole;   // set by plan_paged_attn_prefix
+  PagedCacheFp8 kc8, vc8;    // quantised caches in place of kc and vc; last, bf16 calls do not fetch them
 };
 
 struct CacheReadArgs {

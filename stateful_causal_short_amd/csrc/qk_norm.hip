@@ -127,7 +127,7 @@ __device__ __forceinline__ void store_fp8(const float* x, const PagedCacheFp8& c
 // Token blockIdx.x * PER + ..., heads [per blockIdx.y, per (blockIdx.y + 1)) of
 // its query, key and (copied to the cache) value heads.
 template <int HD, int N, bool FP8>
-__global__ __launch_bounds__(kBlock) void qk_norm_rope(QkNormArgs a, int per) {
+__global__ __launch_bounds__(kBlock) void qk_norm_rope(int per, QkNormArgs a) {
   constexpr int L = HD / 8, PER = kBlock / L;
   const int heads = a.nq + a.nkv + (FP8 || a.vc.p ? a.nkv : 0);
   const int64_t t = (int64_t)blockIdx.x * PER + threadIdx.x / L;
@@ -257,9 +257,9 @@ hipError_t launch_hd(const QkNormArgs& a, hipStream_t s) {
   if (blocks > 0x7FFFFFFFLL || ny > 65535) return hipErrorNotSupported;
   const dim3 grid((unsigned)blocks, (unsigned)ny);
   if (per >= 4)
-    hipLaunchKernelGGL((qk_norm_rope<HD, 4, FP8>), grid, dim3(kBlock), 0, s, a, (int)per);
+    hipLaunchKernelGGL((qk_norm_rope<HD, 4, FP8>), grid, dim3(kBlock), 0, s, (int)per, a);
   else
-    hipLaunchKernelGGL((qk_norm_rope<HD, 1, FP8>), grid, dim3(kBlock), 0, s, a, (int)per);
+    hipLaunchKernelGGL((qk_norm_rope<HD, 1, FP8>), grid, dim3(kBlock), 0, s, (int)per, a);
   return hipGetLastError();
 }
 }  // namespace
