@@ -47,18 +47,15 @@ __device__ __forceinline__ T head_sum(T x) {
   return x;
 }
 
-// A lane's values of a query or key head, normalised and turned: `wp` the weights or
-// NULL, half-split pairs (e, 4 + e) or neighbours.
-template <int HD, typename T>
-__device__ __forceinline__ void norm_turn(T* x, float eps, const uint16_t* wp, int d0, int d1, bool turns,
+// A lane's values of a key head that goes to a quantised cache, normalised and turned
+// in fp64: `wp` the weights or NULL, half-split pairs (e, 4 + e) or neighbours.
+template <int L>
+__device__ __forceinline__ void norm_turn(double* x, float eps, const uint16_t* wp, int d0, int d1, bool turns,
                                           bool interleaved, const float* cs, const float* sn) {
-  T ss = 0;
+  double ss = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) ss = fma(x[e], x[e], ss);
-  ss = head_sum<HD / 8>(ss) * (T)(1.f / HD) + eps;
-  T inv;
-  if constexpr (sizeof(T) == 4) inv = rsqrtf(ss);
-  else inv = rsqrt(ss);
+  const double inv = rsqrt(head_sum<L>(ss) * (0.125 / L) + eps);
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] *= inv;
   if (wp) {
@@ -69,20 +66,13 @@ __device__ __forceinline__ void norm_turn(T* x, float eps, const uint16_t* wp, i
     for (int e = 0; e < 8; ++e) x[e] *= wv[e];
   }
   if (!turns) return;
-  if (interleaved) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const T y1 = x[2 * e], y2 = x[2 * e + 1];
-      x[2 * e] = y1 * cs[e] - y2 * sn[e];
-      x[2 * e + 1] = y2 * cs[e] + y1 * sn[e];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const T y1 = x[e], y2 = x[4 + e];
-      x[e] = y1 * cs[e] - y2 * sn[e];
-      x[4 + e] = y2 * cs[e] + y1 * sn[e];
-    }
+  for (int e = 0; e < 4; ++e) {
+    double& z1 = interleaved ? x[2 * e] : x[e];
+    double& z2 = interleaved ? x[2 * e + 1] : x[4 + e];
+    const double y1 = z1, y2 = z2;
+    z1 = y1 * cs[e] - y2 * sn[e];
+    z2 = y2 * cs[e] + y1 * sn[e];
   }
 }
 
@@ -211,7 +201,6 @@ __global__ __launch_bounds__(kBlock) void qk_norm_rope(int per, QkNormArgs a) {
       float x[8];
       unpack4(x0[n], x);
       unpack4(x1[n], x + 4);
-      const uint16_t* const wp = (const uint16_t*)(is_q ? a.q_w : a.k_w);
       // A key's codes are rounded once, from 64-bit values. fp32 ones lie on the other
       // side of a tie about once in a million, a step of 2^-3 for an error of 2^-23.
       if constexpr (FP8) {
@@ -219,7 +208,7 @@ __global__ __launch_bounds__(kBlock) void qk_norm_rope(int per, QkNormArgs a) {
           double y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = x[e];
-          norm_turn<HD>(y, a.eps, wp, d0, d1, turns, a.interleaved, cs, sn);
+          norm_turn<L>(y, a.eps, (const uint16_t*)a.k_w, d0, d1, turns, a.interleaved, cs, sn);
           float z[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) z[e] = to_odd(y[e]);
@@ -227,7 +216,36 @@ __global__ __launch_bounds__(kBlock) void qk_norm_rope(int per, QkNormArgs a) {
         }
         if (!is_q && !a.k_out) continue;
       }
-      norm_turn<HD>(x, a.eps, wp, d0, d1, turns, a.interleaved, cs, sn);
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      const float inv = rsqrtf(head_sum<L>(ss) * (1.f / HD) + a.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= inv;
+      if (const uint16_t* wp = (const uint16_t*)(is_q ? a.q_w : a.k_w)) {
+        float wv[8];
+        unpack4(*(const uint2*)(wp + d0), wv);
+        unpack4(*(const uint2*)(wp + d1), wv + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= wv[e];
+      }
+      if (turns) {
+        if (a.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y1 = x[2 * e], y2 = x[2 * e + 1];
+            x[2 * e] = y1 * cs[e] - y2 * sn[e];
+            x[2 * e + 1] = y2 * cs[e] + y1 * sn[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y1 = x[e], y2 = x[4 + e];
+            x[e] = y1 * cs[e] - y2 * sn[e];
+            x[4 + e] = y2 * cs[e] + y1 * sn[e];
+          }
+        }
+      }
       const uint2 y0 = pack4(x), y1 = pack4(x + 4);
       if (is_q || a.k_out) {
         uint16_t* d = is_q ? qo + (int64_t)h * HD : ko + (int64_t)(h - a.nq) * HD;
