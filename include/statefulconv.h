@@ -485,7 +485,7 @@ typedef struct {
 /* sc_qk_norm_rope into a quantised cache (required here). The scale of a head is the
  * smallest power of two, from 2^-126 on, that brings its largest finite value to 448
  * or less; values over it are rounded to the nearest code, ties to even, keys
- * straight from fp32. Infinities and NaN become NaN codes and leave the scale to
+ * straight from fp64. Infinities and NaN become NaN codes and leave the scale to
  * the others. Codes 4-byte aligned, strides a multiple of 4. */
 sc_status sc_qk_norm_rope_fp8(const sc_qk_norm_desc* desc, const void* q, const void* k,
                               const void* v, void* q_out, void* k_out, const void* q_weight,
@@ -519,8 +519,9 @@ sc_status sc_paged_cache_read_fp8(const sc_cache_read_desc* desc, const sc_paged
 
 /* sc_paged_attn_decode over quantised caches: the same rows, visibility and
  * arguments. Scores and weights are fp32 (weights enter the second product as two
- * bf16 parts, 2^-16). Codes 16-byte aligned, strides a multiple of 16; scales
- * 4-byte aligned, strides a multiple of 4. The workspace is its own function's. */
+ * bf16 parts, 2^-16). Codes 16-byte aligned, strides a multiple of 16 and of tokens
+ * below 2^26; scales 4-byte aligned, strides a multiple of 4. The workspace is its
+ * own function's. */
 sc_status sc_paged_attn_fp8_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
                                             int32_t q_len, int32_t max_seq_len, int64_t* bytes);
 sc_status sc_paged_attn_decode_fp8(const sc_paged_attn_desc* desc, const void* q, void* out,

@@ -243,3 +243,8 @@ def test_prefix_token_strides():
     for which in ("kc", "vc"):
         assert prefix(attn_desc(), False, **{which: cache(token_stride=1 << 26)}) == UNSUPPORTED
         assert prefix(attn_desc(), True, **{which: q8(token_stride=1 << 26)}) == UNSUPPORTED
+
+
+def test_decode_token_strides():
+    for which in ("kc", "vc"):
+        assert attn(attn_desc(), **{which: q8(token_stride=1 << 26)}) == UNSUPPORTED

@@ -69,6 +69,7 @@ MANY = [  # nq, nkv, hd, q, requests, lengths, max_seq_len
     (8, 4, 64, 1, 400, "some", 700),
     (16, 4, 128, 2, 70, "long", 0),
     (4, 2, 256, 1, 300, "one", 512),
+    (2, 1, 64, 2, 1030, "few", 0),      # one split, a wave's tiles past 64 and past 128
 ]
 
 
@@ -81,6 +82,7 @@ def test_many_requests_over_codes(case):
     rng = np.random.default_rng(B)
     lens = {"some": rng.integers(0, 90, B),
             "long": np.where(np.arange(B) % 9 == 4, rng.integers(2000, 3300, B), rng.integers(0, 40, B)),
+            "few": np.where(np.arange(B) == 77, 9001, np.where(np.arange(B) == 900, 4289, 3)),
             "one": np.where(np.arange(B) == 250, 129, 1)}[kind].tolist()
     c, table, k, v = paged_fp8(g, lens, nkv, hd, 16, "tokens", rng)
     top = top or max(lens)
@@ -119,6 +121,28 @@ def test_bad_pages_and_late_nans():
     assert bool(rows[hit].isnan().all())
     rows[hit] = want.view(q, nq, hd)[hit].to(BF16)
     check_attn(rows.flatten(1), want, tol)
+
+
+def test_undefined_scale_of_a_later_draft():
+    """A scale byte of 255 and NaN codes in a token that only the last draft sees, as
+    in a place that is still to be written, leave the other rows as they were."""
+    nq, nkv, hd, q = 4, 2, 128, 3
+    print("[gpu] attn fp8 late scale", flush=True)
+    g = torch.Generator().manual_seed(9)
+    lens = [50, 33]
+    c, table, k, v = paged_fp8(g, lens, nkv, hd, 16, "tokens", np.random.default_rng(9))
+    for r, n in enumerate(lens):
+        page, at = table[r, (n - 1) // 16], (n - 1) % 16
+        for x in (0, 2):
+            c[x].view(U8)[page, at] = 0x7F
+            c[x + 1].view(U8)[page, :, at] = 255
+    query = randn(g, 2 * q, nq * hd)
+    out = torch.full((2 * q, nq * hd), 7.5, dtype=BF16, device="cuda")
+    scs().sc_paged_attn_decode_fp8(query.cuda(), out, *c, i32(table), i32(lens), q=q, max_seq_len=64)
+    want, tol = ref(query, k, v, lens, q, hd ** -0.5)
+    for r in range(2):
+        rows = slice(r * q, r * q + q - 1)
+        check_attn(out.cpu()[rows], want[rows], tol[rows])
 
 
 def test_scales_over_their_range():
