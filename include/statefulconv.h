@@ -545,7 +545,7 @@ sc_status sc_paged_attn_decode_fp8(const sc_paged_attn_desc* desc, const void* q
  *   num_groups      (host) >= 0; with 0 both arrays may be NULL
  *   max_prefix_len  (host) <= max_seq_len; the split of the prefixes follows from it
  * block_table rows hold a request's whole cache, its prefix first. Over the prefix,
- * weights are rounded to bf16 (their sum is of the rounded ones); everything else is
+ * weights enter the second product as two bf16 parts (2^-15); everything else is
  * as in sc_paged_attn_decode and sc_paged_attn_decode_fp8. Other arguments, limits
  * and alignment are theirs, and token strides are below 2^26; one workspace function
  * serves both caches. */

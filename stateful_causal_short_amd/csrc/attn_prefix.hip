@@ -17,8 +17,8 @@
 // pass through registers and are widened. Scores are taken transposed, keys as the
 // left operand of 32x32x16 bf16 products: a lane then has 16 scores of one row per 32
 // tokens, its maximum and sum need one exchange with the other half-wave, and rescaling
-// the output is a product by a lane's own factor. The same registers, rounded to bf16,
-// are the right operand of the second product, values transposed x weights, whose
+// the output is a product by a lane's own factor. The same registers, as two bf16
+// parts, are the right operands of the second product, values transposed x weights, whose
 // inner index counts the tokens in the order in which they lie there; the transposing
 // LDS read brings the values' columns in that order.
 //
@@ -31,10 +31,11 @@
 // workspace. Matrix units are busy 44% of the cycles; with no LDS reads, copies or barriers at
 // all it takes 116 us, and the clock falls (2.2 to 2.0 GHz) as they get busier.
 //
-// Weights are rounded to bf16 (by 2^-8 of each at most), and the sum is taken of the
-// rounded ones, so that their mean stays one of the values: the error is that of the
-// values' spread, averaged over the tokens, beside 2^-8 for the output's own rounding.
-// Scores, maxima, sums and outputs are fp32.
+// Weights enter the second product in two bf16 parts, the fp32 weight cut to its first
+// eight bits and the rest rounded: 2^-15 of each at most. One rounded part would halve that
+// product (512 requests on 32,768 tokens 223 us for 271) and cost 2^-8 of each, an error as
+// large as the output's own rounding. The second part is never zero or negative, so that an
+// infinite value stays one. Scores, maxima, sums and outputs are fp32.
 #include "attn_device.hpp"
 #include "fp8_device.hpp"
 
@@ -58,6 +59,8 @@ constexpr int kMostTakenIn = 16;   // prefix parts that workgroups of single req
 // A row's maximum may pass the one that its weights refer to by 2^kSlack before the
 // outputs are rescaled: weights then reach 256, far from any limit of bf16 or fp32.
 constexpr float kSlack = 8.f;
+// A weight's second part is kMore times the weight less its first part, never zero.
+constexpr float kMore = 1.f + 0x1p-20f;
 
 // Tokens of a tile.
 constexpr int tile_tokens(int hd, int waves) { return hd == 64 || (hd == 128 && waves >= 4) ? 64 : 32; }
@@ -334,13 +337,10 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 ? 1 : 2) void attn_prefix(Pag
         for (int i = 0; i < 16; ++i) O[d][i] *= f;
     }
   };
-  constexpr int NW = TB * 8;                          // words of a tile's weights, two in each
+  constexpr int NW = TB * 8;                          // words of a part of a tile's weights, two in each
   struct Two { float x, y; };
   auto exponents = [&](const f32x16* s, int x) SC_INLINE {
     return Two{fmaf(s[x / 8][x % 8 * 2], c, -m), fmaf(s[x / 8][x % 8 * 2 + 1], c, -m)};
-  };
-  auto sum = [&](uint32_t p) SC_INLINE {
-    l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), __builtin_bit_cast(bf16x2, 0x3F803F80u), l, false);
   };
   struct Columns { s16x4 a, b; };
   auto read_v = [&](const uint16_t* V, int n) SC_INLINE {
@@ -354,21 +354,22 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 ? 1 : 2) void attn_prefix(Pag
     O[n % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
                                                        __builtin_bit_cast(bf16x8, pf), O[n % DB], 0, 0, 0);
   };
-  // Both products of a turn, the scores of the next tile (keys Kn) and the values of this one
-  // (V) under its weights, step by step in the order in which they are to be issued: a
+  // The products of a turn, the scores of the next tile (keys Kn) and the values of this one
+  // (V) under each part of its weights, step by step in the order in which they are to be issued: a
   // matrix instruction, the LDS read that a later one needs, and of the weights the
   // exponent of one pair, the power of the pair before and the sum of the one before that,
   // so that no instruction waits for its neighbour. `chore(i)`, of `chores`, is what else a
   // turn has to do, the next tiles' way to LDS. The maximum of the next scores is returned.
   auto products = [&](const uint16_t* Kn, const uint16_t* V, const f32x16* cur, f32x16* next, auto chores,
                       auto chore) SC_INLINE {
-    constexpr int NQ = KS * TB, NV = TB * 2 * DB, AHEAD = 3;
+    // values' steps: one with each part of the weights
+    constexpr int NQ = KS * TB, NV = TB * 2 * DB * 2, AHEAD = 3;
     // steps that take weights; a pair is done two slots after its own, and in time
-    constexpr int NS = NW + 2, ES = NQ + NV * 5 / 8;
-    static_assert((NW + 1) * ES / NS < NQ + (NW / 4 - 1) * DB && 5 * ES / NS < NQ, "weights before their product");
+    constexpr int NS = NW + 2, ES = NQ + NV * 3 / 8;
+    static_assert((NW + 1) * ES / NS < NQ + (NW / 4 - 1) * DB * 2 && 5 * ES / NS < NQ, "weights before their product");
     u32x4 kf[AHEAD];
     Columns vf[AHEAD];
-    uint32_t p[NW];
+    uint32_t p[2][NW];
     Two e[2];
     float top[2] = {kNone, kNone};
     int k_lane = k_at;
@@ -389,15 +390,19 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 ? 1 : 2) void attn_prefix(Pag
         if constexpr (n + AHEAD < NQ) kf[n % AHEAD] = read_k(n + AHEAD);
         else vf[n + AHEAD - NQ] = read_v(V, n + AHEAD - NQ);
       } else {
-        value_step(vf[nv % AHEAD], p, nv);
-        if constexpr (nv + AHEAD < NV) vf[nv % AHEAD] = read_v(V, nv + AHEAD);
+        value_step(vf[nv / 2 % AHEAD], p[nv % 2], nv / 2);
+        if constexpr (nv % 2 == 1 && nv / 2 + AHEAD < NV / 2) vf[nv / 2 % AHEAD] = read_v(V, nv / 2 + AHEAD);
       }
       steps<NS>([&](auto slot) SC_INLINE {
         constexpr int x = slot;
         if constexpr (x * ES / NS == n) {
           if constexpr (x >= 2) {
-            p[x - 2] = pack_bf16(e[x % 2].x, e[x % 2].y);
-            sum(p[x - 2]);
+            const Two y = e[x % 2];
+            const uint32_t ux = __float_as_uint(y.x), uy = __float_as_uint(y.y);
+            p[0][x - 2] = __builtin_amdgcn_perm(uy, ux, 0x07060302u);
+            p[1][x - 2] = pack_bf16(fmaf(y.x, kMore, -__uint_as_float(ux & 0xFFFF0000u)),
+                                    fmaf(y.y, kMore, -__uint_as_float(uy & 0xFFFF0000u)));
+            l += y.x + y.y;
           }
           if constexpr (x >= 1 && x <= NW) e[(x - 1) % 2] = Two{exp2_(e[(x - 1) % 2].x), exp2_(e[(x - 1) % 2].y)};
           if constexpr (x < NW) e[x % 2] = exponents(cur, x);
@@ -531,7 +536,7 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 ? 1 : 2) void attn_prefix(Pag
   }
   turns(std::false_type{});
 
-  l += __shfl_xor(l, 32);
+  l = (l + __shfl_xor(l, 32)) * kMore;
   if (!row_ok) return;
   const int row_parts = a.prefix_splits + a.splits;
   const int64_t n_rows = (int64_t)a.batch * a.nq_tok * a.nq;

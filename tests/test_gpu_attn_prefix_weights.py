@@ -1,0 +1,48 @@
+"""Attention over shared prefixes: how far outputs are from 64-bit values, beyond their
+own rounding to bf16, in every split and join of the parts."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests._fp8 import BF16, F64  # noqa: E402
+from tests.test_gpu_attn import attn_ref, check_attn, i32, randn, scs  # noqa: E402
+from tests.test_gpu_attn_prefix import shared  # noqa: E402
+
+
+def check(got, want, tol, top):
+    """Each value: attn_ref's tolerance, and for weights in two bf16 parts, off by 2^-15
+    each, twice that (the mean is off by theirs and by their sum's) of the largest
+    value. All of them: rounding (want + d) to bf16 leaves, in the mean square, what
+    rounding `want` leaves, and d. The errors of the weights, and of fp32 scores, 2^-20 or
+    less here, average as the values themselves do to outputs near zero: d is 2^-15 of
+    the outputs at most, against 2^-9.2 for the rounding, under 2^-5 of it."""
+    check_attn(got, want, tol + 2.0 ** -14 * top)
+    best = float((want.to(BF16).to(F64) - want).norm())
+    off = float((got.to(F64) - want).norm())
+    assert off <= best * (1 + 2.0 ** -5), off / best
+
+
+CASES = [  # nq, nkv, hd, block, q, requests, prefix, own tokens, layout
+    (16, 4, 128, 16, 1, 70, 1500, 8, "tokens"),
+    (8, 2, 64, 64, 3, 40, 900, 30, "joint"),
+    (4, 1, 256, 16, 1, 33, 700, 50, "heads"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("case", CASES, ids=[f"{c[0]}-{c[1]}-{c[2]}-q{c[4]}-{c[5]}on{c[6]}" for c in CASES])
+def test_weights(case, fp8):
+    nq, nkv, hd, block, q, B, P, own, layout = case
+    print(f"[gpu] prefix weights {case} {fp8}", flush=True)
+    g = torch.Generator().manual_seed(B)
+    rng = np.random.default_rng(B)
+    c, table, lens, k, v = shared(g, [B], [P], rng.integers(q, own + 1, B), nkv, hd, block, layout, fp8, rng)
+    query = randn(g, B * q, nq * hd)
+    out = torch.empty(B * q, nq * hd, dtype=BF16, device="cuda")
+    fn = scs().sc_paged_attn_prefix_fp8 if fp8 else scs().sc_paged_attn_prefix
+    fn(query.cuda(), out, *c, i32(table), i32(lens), i32([0, B]), i32([P]), q=q, max_seq_len=max(lens),
+       max_prefix_len=P)
+    want, tol = attn_ref(query, k, v, lens, q, hd ** -0.5)
+    check(out.cpu(), want, tol, max(float(x.abs().max()) for x in v))
