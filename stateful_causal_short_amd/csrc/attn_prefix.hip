@@ -56,8 +56,9 @@ constexpr int kWaveRows = 32;
 constexpr int kMaxPrefixSplits = 96;
 constexpr int kMaxOwnSplits = 32;
 constexpr int kMostTakenIn = 16;   // prefix parts that workgroups of single requests take in
-// A row's maximum may pass the one that its weights refer to by 2^kSlack before the
-// outputs are rescaled: weights then reach 256, far from any limit of bf16 or fp32.
+// Weights refer to a power of two that is 2^kSlack above their row's maximum when it is set,
+// so that the maximum may grow as much before the outputs are rescaled, and no weight is
+// ever above one: sums and outputs stay as far from fp32's limits as with the maximum itself.
 constexpr float kSlack = 8.f;
 // A weight's second part is kMore times the weight less its first part, never zero.
 constexpr float kMore = 1.f + 0x1p-20f;
@@ -326,8 +327,8 @@ __global__ __launch_bounds__(WAVES * 64, HD == 256 ? 1 : 2) void attn_prefix(Pag
   auto take_max = [&](float top) SC_INLINE {
     const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
     top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * c;
-    if (__any(top > m + kSlack)) {
-      const float mn = fmaxf(m, top);
+    if (__any(top > m)) {
+      const float mn = top > m ? top + kSlack : m;
       const float f = exp2_(m - mn);
       m = mn;
       l *= f;

@@ -46,3 +46,28 @@ def test_weights(case, fp8):
        max_prefix_len=P)
     want, tol = attn_ref(query, k, v, lens, q, hd ** -0.5)
     check(out.cpu(), want, tol, max(float(x.abs().max()) for x in v))
+
+
+@pytest.mark.gpu
+def test_large_values_under_growing_scores():
+    """A score that passes the first tile's by 2^7, over values near fp32's limit. Under
+    weights of 2^-7 and one of 1 the values, 2^124 and every fourth 2^126, sum to less
+    than 2^127; under weights that go on to 2^7 they would pass 2^128."""
+    hd, P, B = 64, 320, 3
+    print("[gpu] prefix large values", flush=True)
+    k = torch.zeros(P + 16, 1, hd, dtype=BF16)
+    k[P - 5, 0, 0] = 7.0
+    v = torch.full((P + 16, 1, hd), 2.0 ** 124, dtype=BF16)
+    v[::4] = 2.0 ** 126
+    query = torch.zeros(B, hd, dtype=BF16)
+    query[:, 0] = 1.0
+    table = np.tile(np.arange(P // 16 + 1), (B, 1))
+    out = torch.empty(B, hd, dtype=BF16, device="cuda")
+    scs().sc_paged_attn_prefix(query.cuda(), out, k.cuda().view(-1, 16, 1, hd), v.cuda().view(-1, 16, 1, hd),
+                               i32(table), i32([P + 1] * B), i32([0, B]), i32([P]), max_seq_len=P + 1,
+                               max_prefix_len=P, scale=float(np.log(2.0)))
+    s = query.to(F64) @ k[:P + 1, 0].to(F64).T * float(np.log(2.0))
+    want = torch.softmax(s, -1) @ v[:P + 1, 0].to(F64)
+    # the rounding, weights to 2^-15 twice, scores below 2^3 and sums to 2^-20
+    tol = (2.0 ** -8 + 2.0 ** -13) * want.abs() + 2.0 ** -13 * 2.0 ** 126
+    assert bool(((out.cpu().to(F64) - want).abs() <= tol).all())
