@@ -474,7 +474,8 @@ sc_status sc_paged_attn_decode(const sc_paged_attn_desc* desc, const void* q, vo
  * scale for each token's head, 2^(byte - 127) in a byte (e8m0): (num_blocks,
  * num_kv_heads, block_size) with a unit stride over a block's tokens. A value is its
  * code times its scale. The library writes bytes 1 .. 247; 0 counts as 2^-127, and
- * rows that see a token with a byte of 255 are undefined. */
+ * rows that see a token with a byte of 255 are undefined. A bf16 value of 248 * 2^120
+ * or more is nearest to the code 256 under 247, which is 2^128: infinite in bf16. */
 typedef struct {
   void* data;              /* (device) */
   int64_t block_stride, token_stride, head_stride;
@@ -503,9 +504,10 @@ typedef struct {
 } sc_cache_read_desc;
 
 /* Reads tokens of a quantised cache back as bf16 rows, exactly but for values
- * below bf16's range: row start_loc[r] + i is token first_tokens[r] + i of request
- * r, for start_loc[r] <= row < start_loc[r + 1]. Tokens outside the block table or in a
- * block outside the cache read as zeros; other rows are left as they were.
+ * outside bf16's range (below 2^-126 to the nearest 2^-133, 2^128 as infinity): row
+ * start_loc[r] + i is token first_tokens[r] + i of request r, for start_loc[r] <= row <
+ * start_loc[r + 1]. Tokens outside the block table or in a block outside the cache read
+ * as zeros; other rows are left as they were.
  *   k_out, v_out (device) (num_rows, num_kv_heads * head_dim) bf16, 16-byte aligned
  *   block_table  (device) int32 (batch, max_blocks)
  *   start_loc    (device) int32 (batch + 1), non-decreasing
@@ -548,7 +550,9 @@ sc_status sc_paged_attn_decode_fp8(const sc_paged_attn_desc* desc, const void* q
  * weights enter the second product as two bf16 parts (2^-15); everything else is
  * as in sc_paged_attn_decode and sc_paged_attn_decode_fp8. Other arguments, limits
  * and alignment are theirs, and token strides are below 2^26; one workspace function
- * serves both caches. */
+ * serves both caches. Quantised keys and values of a prefix enter as bf16, as
+ * sc_paged_cache_read_fp8 reads them: below 2^-126 to the nearest 2^-133, 2^128 as
+ * infinity. */
 sc_status sc_paged_attn_prefix_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
                                                int32_t q_len, int32_t max_seq_len,
                                                int32_t num_groups, int32_t max_prefix_len,

@@ -2,7 +2,7 @@
 //
 //   row starts[r] + t  =  code * 2^(byte - 127) of token first[r] + t of request r
 //
-// exact, as four significant bits and a power of two fit bf16. A thread takes 16
+// exact in bf16's range, as four significant bits and a power of two fit bf16. A thread takes 16
 // codes of a key row and of the value row at once: one 16-byte load each, two
 // stores. Bound by bytes: 1 + 1/head_dim read and 2 written per value. 8 requests of up
 // to 262,143 tokens, 4 heads x 128, 806 MB: 151 us (5.3 TB/s; the loads alone 48, the

@@ -13,12 +13,8 @@
 
 namespace sc {
 
-// x 2^(byte - 127), exact in fp32's range whatever the byte.
-__device__ __forceinline__ float times_scale(float x, uint32_t byte) {
-  return __builtin_amdgcn_ldexpf(x, (int)byte - 127);
-}
-
-// Two codes of a word as bf16 values, times a power of two.
+// Two codes of a word as bf16 values, times a power of two: for every code and byte the
+// product rounded once to bf16, subnormal and infinite ones too.
 __device__ __forceinline__ uint32_t fp8_pair_lo(uint32_t w, float by = 1.f) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, by, false));
 }
@@ -31,27 +27,14 @@ __device__ __forceinline__ u32x4 fp8_to_bf16(uint32_t w0, uint32_t w1, float by 
   return u32x4{fp8_pair_lo(w0, by), fp8_pair_hi(w0, by), fp8_pair_lo(w1, by), fp8_pair_hi(w1, by)};
 }
 
-// A scale as the float whose exponent the conversions take.
+// A scale as the float whose exponent the conversions take; that of 0 counts as 2^-127.
 __device__ __forceinline__ float scale_float(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Sixteen codes times their scale: by the conversion itself where no product leaves
-// the normal range, else through fp32.
+// Sixteen codes times their scale.
 __device__ __forceinline__ void fp8_to_bf16_scaled(u32x4 w, uint32_t byte, u32x4* y) {
-  if (byte - 16u < 224u) {
-    const float by = scale_float(byte);
-    y[0] = fp8_to_bf16(w[0], w[1], by);
-    y[1] = fp8_to_bf16(w[2], w[3], by);
-    return;
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t p = e & 1 ? fp8_pair_hi(w[h * 2 + e / 2]) : fp8_pair_lo(w[h * 2 + e / 2]);
-      f32x2 f = {times_scale(__uint_as_float(p << 16), byte),
-                 times_scale(__uint_as_float(p & 0xFFFF0000u), byte)};
-      y[h][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
-    }
+  const float by = scale_float(byte);
+  y[0] = fp8_to_bf16(w[0], w[1], by);
+  y[1] = fp8_to_bf16(w[2], w[3], by);
 }
 
 // The scale's byte for a head whose largest finite value has these bits (no sign):

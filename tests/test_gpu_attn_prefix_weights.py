@@ -5,7 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests._fp8 import BF16, F64  # noqa: E402
+from tests._fp8 import BF16, F64, U8, caches_fp8, put  # noqa: E402
 from tests.test_gpu_attn import attn_ref, check_attn, i32, randn, scs  # noqa: E402
 from tests.test_gpu_attn_prefix import shared  # noqa: E402
 
@@ -71,3 +71,37 @@ def test_large_values_under_growing_scores():
     # the rounding, weights to 2^-15 twice, scores below 2^3 and sums to 2^-20
     tol = (2.0 ** -8 + 2.0 ** -13) * want.abs() + 2.0 ** -13 * 2.0 ** 126
     assert bool(((out.cpu().to(F64) - want).abs() <= tol).all())
+
+
+@pytest.mark.gpu
+def test_scales_over_their_range_in_a_prefix():
+    """Keys of size 2^-120, some under the byte 0, and values of 2^122, one under the byte
+    247. Codes enter the products as bf16, exactly but below 2^-126, where half a step is
+    2^-134: a score is off by that times its query's sum."""
+    hd, nq, P, B = 128, 2, 80, 3
+    print("[gpu] prefix scales", flush=True)
+    g = torch.Generator().manual_seed(5)
+    blocks = P // 16 + 1
+    c = caches_fp8("tokens", blocks, 16, 1, hd)
+    k, v = [], []
+    for b in range(blocks):
+        x = (torch.randn(16, 1, hd, generator=g) * 2.0 ** -120).to(BF16)
+        y = (torch.randn(16, 1, hd, generator=g) * 2.0 ** 122).to(BF16)
+        if b == 2:
+            y[7] = 1.875 * 2.0 ** 127
+        k.append(put(c[0], c[1], b, 0, x))
+        v.append(put(c[2], c[3], b, 0, y))
+    assert int(c[3][2, 0, 7]) == 247 and int(c[1].view(U8).max()) == 1
+    c[1].view(U8)[1, 0, :5] = 0
+    k[1][:5] /= 2
+    n = P + 1
+    k, v = torch.cat(k)[:n], torch.cat(v)[:n]
+    query = (torch.randn(B, nq * hd, generator=g) * 2.0 ** 119).to(BF16)
+    out = torch.empty(B, nq * hd, dtype=BF16, device="cuda")
+    table = np.tile(np.arange(blocks), (B, 1))
+    scs().sc_paged_attn_prefix_fp8(query.cuda(), out, *c, i32(table), i32([n] * B), i32([0, B]), i32([P]),
+                                   max_seq_len=n, max_prefix_len=P)
+    want, tol = attn_ref(query, [k] * B, [v] * B, [n] * B, 1, hd ** -0.5)
+    top = float(v.abs().max())
+    off = 2.0 ** -134 * float(query.to(F64).abs().view(B, nq, hd).sum(-1).max()) * hd ** -0.5
+    check_attn(out.cpu(), want, tol + (2.0 ** -14 + 2 * off) * top)
