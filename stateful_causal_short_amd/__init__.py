@@ -868,26 +868,11 @@ def _paged_fp8(cache, scale, name, blocks, block_size, nkv, hd):
         sc[1] if nkv > 1 else 0)
 
 
-def _caches(k_cache, k_scale, v_cache, v_scale, nkv, hd, dtype):
-    """Blocks, block size and packed descriptors of a pair of caches, quantised if
-    they have scales."""
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
-    blocks, block_size = k_cache.shape[:2]
-    if k_scale is None:
-        kc = _paged(k_cache, "k_cache", blocks, block_size, nkv, hd, dtype)
-        vc = _paged(v_cache, "v_cache", blocks, block_size, nkv, hd, dtype)
-    else:
-        kc = _paged_fp8(k_cache, k_scale, "k", blocks, block_size, nkv, hd)
-        vc = _paged_fp8(v_cache, v_scale, "v", blocks, block_size, nkv, hd)
-    return blocks, block_size, kc, vc
-
-
 def _norm_call(name, query, key, value, q_out, k_out, q_weight, k_weight, cos_sin, positions,
                slots, k_cache, k_scale, v_cache, v_scale, head_dim, eps, interleaved, stream):
     """Marshals a norm, rotation and cache write, into either cache."""
     torch = _torch()
-    if query.dim() != 2 or key.dim() != 2:
+    if query.ndim != 2 or key.ndim != 2:
         raise ValueError("query, key: expected 2-D tensors")
     T, qw = query.shape
     kw = key.shape[1]
@@ -905,12 +890,20 @@ def _norm_call(name, query, key, value, q_out, k_out, q_weight, k_weight, cos_si
     if k_cache is None:
         value = slots = None
     else:
+        pool = k_cache.shape
+        if len(pool) != 4:
+            raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
         if value is None or slots is None:
             raise ValueError("value, slots: expected with the caches")
-        blocks, block_size, kc, vc = _caches(k_cache, k_scale, v_cache, v_scale, nkv, head_dim,
-                                             dtype)
+        blocks, block_size = pool[0], pool[1]
+        if k_scale is None:
+            kc = _paged(k_cache, "k_cache", blocks, block_size, nkv, head_dim, dtype)
+            vc = _paged(v_cache, "v_cache", blocks, block_size, nkv, head_dim, dtype)
+        else:
+            kc = _paged_fp8(k_cache, k_scale, "k", blocks, block_size, nkv, head_dim)
+            vc = _paged_fp8(v_cache, v_scale, "v", blocks, block_size, nkv, head_dim)
         v_rs = _row_stride(value, "value", kw, T, dtype)
-        if slots.dtype != torch.int64 or slots.dim() != 1 or slots.shape[0] < T or \
+        if slots.dtype != torch.int64 or slots.ndim != 1 or slots.shape[0] < T or \
                 not slots.is_contiguous():
             raise ValueError(f"slots: expected a contiguous int64 tensor of {T} entries")
     rot, t_rs, top, t_code = 0, 0, 0, SC_DTYPE_F32
@@ -919,7 +912,7 @@ def _norm_call(name, query, key, value, q_out, k_out, q_weight, k_weight, cos_si
     else:
         top, rot = cos_sin.shape
         t_rs, t_code = _row_stride(cos_sin, "cos_sin", rot, top, cos_sin.dtype), _dtype_code(cos_sin)
-        if positions is None or positions.dtype != torch.int64 or positions.dim() != 1 or \
+        if positions is None or positions.dtype != torch.int64 or positions.ndim != 1 or \
                 positions.shape[0] < T or not positions.is_contiguous():
             raise ValueError(f"positions: expected a contiguous int64 tensor of {T} entries")
     desc = _QK_NORM_DESC.pack(
@@ -927,8 +920,11 @@ def _norm_call(name, query, key, value, q_out, k_out, q_weight, k_weight, cos_si
         eps, block_size, blocks, _row_stride(query, "query", qw, T, dtype),
         _row_stride(key, "key", kw, T, dtype), v_rs, _row_stride(q_out, "q_out", qw, T, dtype),
         0 if k_out is None else _row_stride(k_out, "k_out", kw, T, dtype), t_rs, top)
-    ptr = _addresses(_device(query), query, key, value, q_out, k_out, q_weight, k_weight, cos_sin,
-                     positions, slots, k_cache, v_cache, k_scale, v_scale)
+    dev = _device(query)
+    ptr = _addresses(dev, query, key, value, q_out, k_out, q_weight, k_weight, cos_sin, positions,
+                     slots, k_cache, v_cache)
+    if k_scale is not None:
+        _addresses(dev, k_scale, v_scale)
     st = getattr(lib(), name)(desc, *ptr[:10], kc, vc, T, _stream(stream, query))
     if st != SC_OK:
         raise ScError(name, st)
@@ -995,7 +991,7 @@ def sc_paged_cache_read_fp8(k_cache, k_scale, v_cache, v_scale, k_out, v_out, bl
     torch = _torch()
     if k_cache.dim() != 4:
         raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
-    nkv, hd = k_cache.shape[2:]
+    blocks, block_size, nkv, hd = k_cache.shape
     if k_out.dim() != 2:
         raise ValueError("k_out: expected a 2-D tensor")
     if start_loc.dim() != 1 or start_loc.shape[0] < 1:
@@ -1005,8 +1001,8 @@ def sc_paged_cache_read_fp8(k_cache, k_scale, v_cache, v_scale, k_out, v_out, bl
     t_rs, width = _block_table(block_table, batch)
     if first_tokens is not None:
         _counts(first_tokens, "first_tokens", batch)
-    blocks, block_size, kc, vc = _caches(k_cache, _given(k_scale, "k_scale"), v_cache,
-                                         _given(v_scale, "v_scale"), nkv, hd, None)
+    kc = _paged_fp8(k_cache, _given(k_scale, "k_scale"), "k", blocks, block_size, nkv, hd)
+    vc = _paged_fp8(v_cache, _given(v_scale, "v_scale"), "v", blocks, block_size, nkv, hd)
     desc = _CACHE_READ_DESC.pack(
         nkv, hd, block_size, blocks, _row_stride(k_out, "k_out", nkv * hd, rows, torch.bfloat16),
         _row_stride(v_out, "v_out", nkv * hd, rows, torch.bfloat16), t_rs)
@@ -1061,15 +1057,17 @@ def sc_paged_attn_prefix_workspace_bytes(batch: int, *, q: int = 1, max_seq_len:
 
 
 def _attn_call(name, need, query, out, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens,
-               max_seq_len, q, scale, workspace, stream, groups=(), sizes=()):
-    """Marshals an attention call over either cache; `groups` and `sizes` are what one
-    with shared prefixes has besides."""
-    if k_cache.dim() != 4:
+               max_seq_len, q, scale, workspace, stream, groups=None):
+    """Marshals an attention call over either cache; `groups`: (group_start_loc,
+    prefix_lens, their number, max_prefix_len) of one with shared prefixes. The checks
+    stand here one after another: a decode step is as long as its marshalling."""
+    torch = _torch()
+    pool, shape = k_cache.shape, query.shape
+    if len(pool) != 4:
         raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
-    nkv, hd = k_cache.shape[2:]
-    if query.dim() != 2:
+    if len(shape) != 2:
         raise ValueError("query: expected a 2-D tensor")
-    rows, qw = query.shape
+    (blocks, block_size, nkv, hd), (rows, qw) = pool, shape
     if hd < 1 or qw % hd or qw == 0:
         raise ValueError(f"query: expected rows of heads of {hd} values")
     if q < 1 or rows % q:
@@ -1077,26 +1075,50 @@ def _attn_call(name, need, query, out, k_cache, k_scale, v_cache, v_scale, block
     if not 0 <= max_seq_len < 1 << 31:
         raise ValueError("max_seq_len: expected 0 .. 2^31 - 1")
     batch, dtype = rows // q, query.dtype
-    t_rs, width = _block_table(block_table, batch)
-    _counts(seq_lens, "seq_lens", batch)
-    blocks, block_size, kc, vc = _caches(k_cache, k_scale, v_cache, v_scale, nkv, hd, dtype)
+    table = block_table.shape
+    if len(table) != 2 or table[0] < batch or block_table.dtype != torch.int32:
+        raise ValueError(f"block_table: expected int32 ({batch}, max_blocks)")
+    t_rs, t_cs = block_table.stride()
+    if table[1] > 1 and t_cs != 1 and table[0]:
+        raise ValueError("block_table: expected adjacent entries in a row")
+    if seq_lens.dtype != torch.int32 or seq_lens.ndim != 1 or seq_lens.shape[0] < batch or \
+            not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens: expected a contiguous int32 tensor of {batch} entries")
     desc = _ATTN_DESC.pack(
         qw // hd, nkv, hd, _dtype_code(query), block_size, blocks,
         hd ** -0.5 if scale is None else scale, _row_stride(query, "query", qw, rows, dtype),
-        _row_stride(out, "out", qw, rows, dtype), t_rs)
+        _row_stride(out, "out", qw, rows, dtype), t_rs if table[0] > 1 else max(table[1], 1))
+    if k_scale is None:
+        kc = _paged(k_cache, "k_cache", blocks, block_size, nkv, hd, dtype)
+        vc = _paged(v_cache, "v_cache", blocks, block_size, nkv, hd, dtype)
+    else:
+        kc = _paged_fp8(k_cache, k_scale, "k", blocks, block_size, nkv, hd)
+        vc = _paged_fp8(v_cache, v_scale, "v", blocks, block_size, nkv, hd)
     dev = _device(query)
     raw = _stream(stream, query)
+    library = lib()
     if workspace is None:
-        workspace = _workspace(None, _workspace_need(need, desc, batch, q, max_seq_len, *sizes),
-                               query, stream)
+        sizes = (batch, q, max_seq_len) if groups is None else (batch, q, max_seq_len, *groups[2:])
+        n = ctypes.c_int64(0)
+        st = getattr(library, need)(desc, *sizes, ctypes.byref(n))
+        if st != SC_OK:
+            raise ScError(need, st)
+        if n.value:
+            workspace = _workspace(None, n.value, query, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ptr = _addresses(dev, query, out, block_table, seq_lens, workspace, k_cache, v_cache)
+    if k_scale is not None:
+        _addresses(dev, k_scale, v_scale)
+    if groups is None:
+        st = getattr(library, name)(desc, ptr[0], ptr[1], kc, vc, ptr[2], table[1], ptr[3], batch,
+                                    q, max_seq_len, ptr[4], nbytes, raw)
     else:
-        _workspace(workspace, 0, query, stream)
-    ptr = _addresses(dev, query, out, block_table, seq_lens, workspace, *groups, k_cache, v_cache,
-                     k_scale, v_scale)
-    # (groups' arrays, their number, batch, q, max_seq_len, longest prefix)
-    more = (*ptr[5:5 + len(groups)], *sizes[:1], batch, q, max_seq_len, *sizes[1:])
-    st = getattr(lib(), name)(desc, ptr[0], ptr[1], kc, vc, ptr[2], width, ptr[3], *more, ptr[4],
-                              _nbytes(workspace), raw)
+        starts, lens, n_groups, longest = groups
+        st = getattr(library, name)(desc, ptr[0], ptr[1], kc, vc, ptr[2], table[1], ptr[3],
+                                    *_addresses(dev, starts, lens), n_groups, batch, q,
+                                    max_seq_len, longest, ptr[4], nbytes, raw)
     if st != SC_OK:
         raise ScError(name, st)
 
@@ -1140,7 +1162,7 @@ def _prefix_call(name, query, out, k_cache, k_scale, v_cache, v_scale, block_tab
         raise ValueError("max_prefix_len: expected 0 .. 2^31 - 1")
     _attn_call(name, "sc_paged_attn_prefix_workspace_bytes", query, out, k_cache, k_scale, v_cache,
                v_scale, block_table, seq_lens, max_seq_len, q, scale, workspace, stream,
-               (group_start_loc, prefix_lens), (groups, max_prefix_len))
+               (group_start_loc, prefix_lens, groups, max_prefix_len))
 
 
 def sc_paged_attn_prefix(query, out, k_cache, v_cache, block_table, seq_lens, group_start_loc,
