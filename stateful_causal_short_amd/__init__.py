@@ -989,6 +989,10 @@ def sc_paged_cache_read_fp8(k_cache, k_scale, v_cache, v_scale, k_out, v_out, bl
     or None: from the first token on. Caches as for sc_qk_norm_rope_fp8.
     """
     torch = _torch()
+    for t, name in ((k_cache, "k_cache"), (k_scale, "k_scale"), (v_cache, "v_cache"),
+                    (v_scale, "v_scale"), (k_out, "k_out"), (v_out, "v_out"),
+                    (block_table, "block_table"), (start_loc, "start_loc")):
+        _given(t, name)
     if k_cache.dim() != 4:
         raise ValueError("k_cache: expected (num_blocks, block_size, nkv, head_dim)")
     blocks, block_size, nkv, hd = k_cache.shape
@@ -1001,8 +1005,8 @@ def sc_paged_cache_read_fp8(k_cache, k_scale, v_cache, v_scale, k_out, v_out, bl
     t_rs, width = _block_table(block_table, batch)
     if first_tokens is not None:
         _counts(first_tokens, "first_tokens", batch)
-    kc = _paged_fp8(k_cache, _given(k_scale, "k_scale"), "k", blocks, block_size, nkv, hd)
-    vc = _paged_fp8(v_cache, _given(v_scale, "v_scale"), "v", blocks, block_size, nkv, hd)
+    kc = _paged_fp8(k_cache, k_scale, "k", blocks, block_size, nkv, hd)
+    vc = _paged_fp8(v_cache, v_scale, "v", blocks, block_size, nkv, hd)
     desc = _CACHE_READ_DESC.pack(
         nkv, hd, block_size, blocks, _row_stride(k_out, "k_out", nkv * hd, rows, torch.bfloat16),
         _row_stride(v_out, "v_out", nkv * hd, rows, torch.bfloat16), t_rs)
@@ -1146,13 +1150,17 @@ def sc_paged_attn_decode_fp8(query, out, k_cache, k_scale, v_cache, v_scale, blo
     """sc_paged_attn_decode over quantised caches (as for sc_qk_norm_rope_fp8); its
     workspace has sc_paged_attn_fp8_workspace_bytes bytes."""
     _attn_call("sc_paged_attn_decode_fp8", "sc_paged_attn_fp8_workspace_bytes", query, out,
-               k_cache, _given(k_scale, "k_scale"), v_cache, _given(v_scale, "v_scale"),
-               block_table, seq_lens, max_seq_len, q, scale, workspace, stream)
+               _given(k_cache, "k_cache"), _given(k_scale, "k_scale"), _given(v_cache, "v_cache"),
+               _given(v_scale, "v_scale"), block_table, seq_lens, max_seq_len, q, scale, workspace,
+               stream)
 
 
 def _prefix_call(name, query, out, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens,
                  group_start_loc, prefix_lens, max_seq_len, max_prefix_len, q, scale, workspace,
                  stream):
+    for t, given in ((k_cache, "k_cache"), (v_cache, "v_cache"),
+                     (group_start_loc, "group_start_loc"), (prefix_lens, "prefix_lens")):
+        _given(t, given)
     if prefix_lens.dim() != 1:
         raise ValueError("prefix_lens: expected a 1-D tensor")
     groups = prefix_lens.shape[0]
