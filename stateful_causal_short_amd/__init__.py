@@ -1183,7 +1183,8 @@ def sc_paged_attn_prefix(query, out, k_cache, v_cache, block_table, seq_lens, gr
     group_start_loc[g+1]); prefix_lens int32 (G): their first tokens that are the
     same, at most max_prefix_len. block_table rows hold whole caches, the prefix
     first; requests too short to see the whole prefix, and those of no group, are
-    taken by themselves. workspace: None, or a tensor of
+    taken by themselves (long ones beside large groups end sooner in a call of
+    sc_paged_attn_decode). workspace: None, or a tensor of
     sc_paged_attn_prefix_workspace_bytes bytes. The other arguments are those of
     sc_paged_attn_decode.
     """

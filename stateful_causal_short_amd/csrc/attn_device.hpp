@@ -14,6 +14,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kTile = 16;        // cached tokens per tile
 constexpr int kRows = 16;        // query rows per workgroup of a split
 constexpr int kMaxSplits = 64;
+constexpr int kOwnLeast = 256;   // tokens behind a prefix, a multiple of both kernels' turns
 constexpr int kSortMax = 512;    // requests put in order by their workgroups
 constexpr float kNone = -3.402823466e38f;   // running maximum before any token, the lowest value
 
@@ -81,11 +82,11 @@ __device__ __forceinline__ int shared_tokens(const PagedAttnArgs& a, int r, int 
   return n <= len - a.nq_tok + 1 ? n : 0;
 }
 
-// Tokens [lo, hi) of a split of a request's own part, which begins at `start`:
-// equal parts of whole turns of `unit` tokens, from a multiple of 16 on.
+// Tokens of a split of a request's own part, which begins at `start`: equal parts of
+// whole turns of `unit` tokens, from a multiple of 16 on, kOwnLeast or more.
 __device__ __forceinline__ int own_split_len(const PagedAttnArgs& a, int start, int len, int unit) {
   const int units = (max(len - (start & ~15), 0) + unit - 1) / unit;
-  return max(1, (units + a.splits - 1) / a.splits) * unit;
+  return max((units + a.splits - 1) / a.splits * unit, kOwnLeast);
 }
 
 // What the attn_prefix workgroups left of rows whose own tokens a workgroup of four waves

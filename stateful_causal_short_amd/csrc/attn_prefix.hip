@@ -715,10 +715,18 @@ int64_t plan_paged_attn_prefix(PagedAttnArgs* a, bool fp8) {
   a->prefix_split_len = (int32_t)(per * tn);
   a->row_tiles = (int32_t)std::min<int64_t>(tiles, 0x7FFFFFFF);
   // Splits of the requests' own tokens: as in plan_paged_attn, for the length that is
-  // left behind the longest prefix. A longer rest is cut into as many, longer, parts.
+  // left behind the longest prefix. A longer rest is cut into as many, longer, parts. Where
+  // few rows leave so many parts of the prefix that a launch of its own joins them, a longer
+  // rest would keep its workgroups alone on the card: there the split is for whole caches
+  // of own tokens, up to four workgroups a CU, and those behind a short rest end at once. 8
+  // requests on 32,768 tokens, 16 query and 4 key/value heads x 128, and 4 of 32,000 of no
+  // group: 732 us without, 82 with (quantised 319 and 59; by sc_paged_attn_decode 110); the
+  // 8 alone 31 us either way. With more rows the split would cost each batch a join, 64 x 4
+  // drafts on 16,384 tokens 82 us for 86 and ten groups 58 for 63, long rest or not.
   const int64_t base = (int64_t)a->batch * a->nkv * ((rows_each + kRows - 1) / kRows);
-  const int64_t left = a->max_len - a->max_prefix + kTile;
-  const int64_t want = base >= 4 * cus ? 8 * cus : 16 * cus;
+  const bool every = a->prefix_splits > kMostTakenIn;
+  const int64_t left = every ? a->max_len : a->max_len - a->max_prefix + kTile;
+  const int64_t want = every ? 4 * cus : base >= 4 * cus ? 8 * cus : 16 * cus;
   a->splits = (int32_t)std::max<int64_t>(
       1, std::min<int64_t>({(want + base - 1) / base, (left + 1023) / 1024, kMaxOwnSplits}));
   // One split of them takes the prefix's parts in by itself, a wave a fourth of them.
