@@ -520,10 +520,9 @@ sc_status sc_paged_cache_read_fp8(const sc_cache_read_desc* desc, const sc_paged
                                   int32_t batch, int64_t num_rows, void* stream);
 
 /* sc_paged_attn_decode over quantised caches: the same rows, visibility and
- * arguments. Scores and weights are fp32 (weights enter the second product as two
- * bf16 parts, 2^-16). Codes 16-byte aligned, strides a multiple of 16 and of tokens
- * below 2^26; scales 4-byte aligned, strides a multiple of 4. The workspace is its
- * own function's. */
+ * arguments, scores and weights in fp32. Codes 16-byte aligned, strides a multiple of
+ * 16 and of tokens below 2^26; scales 4-byte aligned, strides a multiple of 4. The
+ * workspace is its own function's. */
 sc_status sc_paged_attn_fp8_workspace_bytes(const sc_paged_attn_desc* desc, int32_t batch,
                                             int32_t q_len, int32_t max_seq_len, int64_t* bytes);
 sc_status sc_paged_attn_decode_fp8(const sc_paged_attn_desc* desc, const void* q, void* out,

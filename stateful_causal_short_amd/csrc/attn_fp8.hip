@@ -14,8 +14,9 @@
 // two score tiles then are the left operand of a 16x16x32 product with the values, if
 // its inner index counts a lane's four tokens of the first tile, then of the second.
 // For that product a lane's values are turned from rows into columns, two tokens to a
-// register, by byte permutes before the codes are widened. The weights enter as two
-// bf16 parts of their fp32 values (2^-16), which is more than the output keeps.
+// register, by byte permutes before the codes are widened. The weights enter as three
+// bf16 parts, all of an fp32 value's bits: 118.3 us for 117.8 with two, 2^-16 of each
+// weight (512 requests below), 89.5 for 89.0 (drafts).
 //
 // 16 query and 4 key/value heads x 128: 512 requests of up to 2,048 tokens, 545 MB, 114 to
 // 120 us (4.7 TB/s); 3 of 131,071, 406 MB, 82 to 92 (4.4 to 4.9) and the join's 6; 64 x 4
@@ -237,8 +238,8 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
         for (int d = 0; d < VPL; ++d) O[d][i] *= fi;
       }
     }
-    // the weights times the values' scales, in two parts
-    u32x4 hi, lo;
+    // the weights times the values' scales, in three parts
+    u32x4 part[3];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -247,10 +248,12 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
         l += p0;
         l += p1;
         f32x2 y = {p0 * scale_of(cur.vs[u], i), p1 * scale_of(cur.vs[u], i + 1)};
-        const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2));
-        f32x2 z = {y[0] - __uint_as_float(h << 16), y[1] - __uint_as_float(h & 0xFFFF0000u)};
-        hi[u * 2 + i / 2] = h;
-        lo[u * 2 + i / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(z, bf16x2));
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2));
+          part[x][u * 2 + i / 2] = h;
+          y = f32x2{y[0] - __uint_as_float(h << 16), y[1] - __uint_as_float(h & 0xFFFF0000u)};
+        }
       }
     // Value rows that no row of the tile sees hold anything, NaN codes included,
     // which a weight of 0 would not undo: they count as zeros. So do NaN codes that
@@ -296,10 +299,10 @@ __global__ __launch_bounds__(kBlock, HD == 256 ? 2 : HD == 128 ? 3 : 4) void att
 #pragma unroll
         for (int y = 0; y < 4; ++y) v[y] = e & 1 ? fp8_pair_hi(col[y]) : fp8_pair_lo(col[y]);
         f32x4& o = O[x * 4 + e];
-        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, hi),
-                                                    __builtin_bit_cast(bf16x8, v), o, 0, 0, 0);
-        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, lo),
-                                                    __builtin_bit_cast(bf16x8, v), o, 0, 0, 0);
+#pragma unroll
+        for (int y = 0; y < 3; ++y)
+          o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, part[y]),
+                                                      __builtin_bit_cast(bf16x8, v), o, 0, 0, 0);
       }
     }
     if (more) {
