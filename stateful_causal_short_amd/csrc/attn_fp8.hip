@@ -19,11 +19,11 @@
 // weight (512 requests below), 89.5 for 89.0 (drafts).
 //
 // 16 query and 4 key/value heads x 128: 512 requests of up to 2,048 tokens, 545 MB, 114 to
-// 120 us (4.7 TB/s); 3 of 131,071, 406 MB, 82 to 92 (4.4 to 4.9) and the join's 6; 64 x 4
-// drafts of up to 8,192, 273 MB, 68 to 82 and 7. The same loads without the products and
-// sums take 112, 78 and 66: neither 32-byte runs of a key per lane nor streaming loads
-// changed that. Registers are loaded again right after their last use; 162 of them let three
-// waves run on a SIMD.
+// 121 us (4.6 TB/s); 3 of 131,071, 406 MB, 82 to 92 (4.4 to 4.9) and the join's 6; 64 x 4
+// drafts of up to 8,192, 273 MB, 68 to 82 and 7; sessions differ. In one session the same
+// loads without the products and sums took 112, 78 and 66: neither 32-byte runs of a key per
+// lane nor streaming loads changed that. Registers are loaded again right after their last
+// use; 164 of them let three waves run on a SIMD.
 #include "attn_device.hpp"
 #include "fp8_device.hpp"
 

@@ -23,13 +23,14 @@
 // LDS read brings the values' columns in that order.
 //
 // Matrix instructions and exponentials take about the same time: scores run a tile
-// ahead, and both products' instructions are issued with the exponentials, LDS reads,
+// ahead, and the products' instructions are issued with the exponentials, LDS reads,
 // sums and the next tiles' copies between them. 2,048 rows x 4 key/value heads x 128 on
-// 32,768 tokens: 148 us, 928 TFLOP/s (a large bf16 library product reaches 1,158 here);
-// with the compiler's order 187, with this order and tiles through registers 174, with
-// copies that stop the counters of LDS reads 153. 7 us of it are the parts' way to the
-// workspace. Matrix units are busy 44% of the cycles; with no LDS reads, copies or barriers at
-// all it takes 116 us, and the clock falls (2.2 to 2.0 GHz) as they get busier.
+// 32,768 tokens: 194 us, 208 GFLOP with both parts of the weights, 1,070 TFLOP/s (a large
+// bf16 library product reaches 1,158 here). Of weights in one part, 139 GFLOP, it took
+// 146 us so; with the compiler's order 187, with this order and tiles through registers
+// 174, with copies that stop the counters of LDS reads 153, with no LDS reads, copies or
+// barriers at all 116. 7 us are the parts' way to the workspace. Matrix units are busy 52%
+// of the cycles, and the clock falls (2.2 to 2.0 GHz) as they get busier.
 //
 // Weights enter the second product in two bf16 parts, the fp32 weight cut to its first
 // eight bits and the rest rounded: 2^-15 of each at most. One rounded part would halve that
@@ -648,13 +649,23 @@ namespace {
 
 // About how long attn_prefix and the way of its parts take (us) with `splits` of the
 // prefix and `waves` in a workgroup. Measured, 64 tokens x 128: a tile takes 0.9 us (0.6
-// with 32 tokens) and 0.17 for each busy wave on its CU, widening codes 0.17 for each
-// workgroup of fewer than eight waves there; a call 7 us to begin and end, a part 1 us for
-// each 2 MB there and back, a join launch 4; the prefix comes at 5.5 TB/s. So for 256 rows x
-// 4 heads on 16,384 tokens 4 waves and 32 splits are taken, 38 us (8 and 32: 42, 4 and
-// 16: 41); for 1,024 rows on 4,096 4 and 8, 41 us (8 and 16: 43, 4 and 16: 43); for 2,048 on
-// 32,768 8 and 8, 220 us (4 and 4: 276); for 10 groups of 201 requests x 8 rows x 64 on up
-// to 8,192 2 and 8, 50 us (4 and 5: 55, 8 and 4: 61).
+// with 32 tokens, but of 256-wide heads) and 0.24 for each busy wave on its CU, widening
+// codes 0.17 for each workgroup of fewer than eight waves there; a call 7 us to begin and
+// end, a part 1 us for each 2 MB there and back, a join launch 4; the prefix comes at 5.5
+// TB/s. What is taken (waves / splits) and others, us for the call with 16 own tokens or
+// fewer; rows of each of 4 heads:
+//   256 rows x 128 on 16,384      4 / 32  37   (8 / 32  44, 4 / 16  43, 4 / 64  39, 2 / 64  41)
+//   1,024 on 4,096                4 / 8   37   (8 / 16  39, 4 / 16  39, 2 / 16  39)
+//   2,048 on 32,768               8 / 8  203   (8 / 16 219, 4 / 8  209, 4 / 4  227)
+//   1,024 on 16,384, quantised    8 / 16  73   (8 / 8  100, 4 / 16  77, 4 / 8   83)
+//   32 on 1,024                   8 / 16  16   (8 / 8   15, 4 / 8   16, 2 / 8   16)
+//   201 x 8 x 64 in ten groups    2 / 8   47   (4 / 16  56, 8 / 5   56, 2 / 16  52)
+//   512 x 64 on 8,192             4 / 16  26   (8 / 16  31, 4 / 32  33, 2 / 16  31)
+//   4,096 x 64 on 8,192           8 / 4   77   (8 / 8   84, 4 / 4   78, 4 / 8   81)
+//   256 x 256 on 8,192            2 / 16  47   (4 / 16  51, 4 / 32  45, 2 / 32  46)
+//   2,048 x 256 on 8,192          4 / 4  147   (4 / 8  166, 2 / 4  153, 2 / 8  168)
+//   32 x 256 on 16,384            4 / 64  33   (4 / 32  43, 4 / 96  44, 2 / 96  34)
+//   1,024 x 256, quantised        4 / 8   91   (4 / 16 111, 2 / 8  106, 4 / 4  148)
 struct PrefixTime {
   PrefixTime(const PagedAttnArgs& a, int waves, int64_t rows, int64_t groups, bool fp8) {
     cus = device_cus();
@@ -665,7 +676,7 @@ struct PrefixTime {
     slots = (a.hd == 256 ? 4 : 8) / waves * cus;
     base_us = tn == 64 || a.hd == 256 ? 0.9 : 0.6;
     // a workgroup's, of its busy waves
-    more_us = 0.17 * tn * a.hd / 8192 * ((double)rows / kWaveRows + groups * 0.5) / tiles +
+    more_us = 0.24 * tn * a.hd / 8192 * ((double)rows / kWaveRows + groups * 0.5) / tiles +
               (fp8 && waves < 8 ? 0.17 : 0);
     read_us = (double)groups * a.max_prefix * a.nkv * a.hd * (fp8 ? 2 : 4) / 5.5e6;
     part_us = (double)rows * a.nkv * a.hd * 4 / 2.2e6;
@@ -723,6 +734,9 @@ int64_t plan_paged_attn_prefix(PagedAttnArgs* a, bool fp8) {
   // group: 732 us without, 82 with (quantised 319 and 59; by sc_paged_attn_decode 110); the
   // 8 alone 31 us either way. With more rows the split would cost each batch a join, 64 x 4
   // drafts on 16,384 tokens 82 us for 86 and ten groups 58 for 63, long rest or not.
+  // Quantised own tokens take the same rule: 4 requests of up to 8,192 behind 1,024, 8 splits
+  // 25 us (16: 21), 16 of up to 4,096, 4 splits 29 us (8: 27), 64 of up to 2,000, 2 splits 42
+  // (1: 44, 4: 43), 256 of them, 2 splits 91 (1: 88, 4: 92).
   const int64_t base = (int64_t)a->batch * a->nkv * ((rows_each + kRows - 1) / kRows);
   const bool every = a->prefix_splits > kMostTakenIn;
   const int64_t left = every ? a->max_len : a->max_len - a->max_prefix + kTile;

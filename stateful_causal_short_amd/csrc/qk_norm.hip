@@ -14,9 +14,10 @@
 // k_out and a cache). 32,768 tokens of 16 + 2 + 2 heads x 128, 355 MB: 84 us
 // (4.2 TB/s; a row copy reaches 5.8). Loading the next heads while these are
 // stored took 90 us, two heads at a time 87, ten 84. 17 tokens: 3.5 us, the
-// latency of three dependent loads. Into a quantised cache, 16 + 4 + 4 heads: 32,768
-// tokens, 373 MB, 82-87 us; 85 with fp32 keys. Two to sixteen times as many workgroups
-// of fewer heads took 85 to 122 us, streaming loads and stores 88. 17 tokens: 4.1 us.
+// latency of three dependent loads. The same heads into a quantised cache: 32,768
+// tokens, 328 MB, 82-87 us (4.0 TB/s); 85 with fp32 keys. Two to sixteen times as many
+// workgroups of fewer heads took 85 to 122 us, streaming loads and stores 88. 17 tokens:
+// 4.2 us.
 #include "attn.hpp"
 #include "common.hpp"
 #include "fp8_device.hpp"
