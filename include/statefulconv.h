@@ -538,12 +538,12 @@ sc_status sc_paged_attn_decode_fp8(const sc_paged_attn_desc* desc, const void* q
  * same keys and values in their first prefix_lens[g] tokens, in the same blocks or
  * copies of them: they are read where the first such request has them whose new
  * tokens all see the whole prefix. Requests whose new tokens do not (short ones,
- * rows that pad a captured batch) and those of no group are taken by themselves,
- * with the results of sc_paged_attn_decode, whatever the others hold. Into how many
- * parts they are split follows from the sizes alone: from max_seq_len where few rows
- * share long prefixes, else from max_seq_len - max_prefix_len, and requests of
- * many thousand tokens that share none of them then end sooner in a call of
- * sc_paged_attn_decode.
+ * rows that pad a captured batch) and those of no group are taken by themselves, as
+ * in sc_paged_attn_decode, whatever the others hold. Into how many parts a request's
+ * own tokens are split follows from the sizes alone: from max_seq_len where few rows
+ * share long prefixes, else from max_seq_len - max_prefix_len. Requests with many
+ * thousand tokens of their own beside large groups end sooner in a call without
+ * groups.
  *   group_start_loc (device) int32 (num_groups + 1), non-decreasing, in [0, batch]
  *   prefix_lens     (device) int32 (num_groups), clamped to [0, max_prefix_len]; any
  *                   length, in whole blocks or not
