@@ -13,7 +13,7 @@ from tests._fp8 import BF16  # noqa: E402
 from tests.test_attn_fp8_host import prefix  # noqa: E402
 from tests.test_attn_host import BIG, INVALID, ODD, UNSUPPORTED, attn_desc  # noqa: E402
 from tests.test_gpu_attn import attn_ref, i32, randn, scs  # noqa: E402
-from tests.test_gpu_attn_prefix import shared  # noqa: E402
+from tests.test_gpu_attn_prefix import CASES as SMALL, shared  # noqa: E402
 from tests.test_gpu_attn_prefix_weights import check  # noqa: E402
 
 
@@ -78,26 +78,42 @@ def test_long_own_parts_are_split(fp8):
     assert parts(fp8, 4, 1, 128, 2, 1, 1_000_050, 1_000_000, 1) >= 96 + 16
 
 
+def run(fp8, nq, nkv, hd, block, q, sizes, prefixes, mine, layout, scale, rng, seed):
+    """One call, checked by check()."""
+    g = torch.Generator().manual_seed(seed)
+    B = sum(sizes)
+    c, table, lens, k, v = shared(g, sizes, prefixes, mine, nkv, hd, block, layout, fp8, rng)
+    query = randn(g, B * q, nq * hd)
+    out = torch.full((B * q + 1, nq * hd), 7.5, dtype=BF16, device="cuda")
+    fn = scs().sc_paged_attn_prefix_fp8 if fp8 else scs().sc_paged_attn_prefix
+    fn(query.cuda(), out, *c, i32(table), i32(lens), i32(np.concatenate([[0], np.cumsum(sizes)])),
+       i32(prefixes), q=q, max_seq_len=max(lens), max_prefix_len=max(prefixes), scale=scale)
+    want, tol = attn_ref(query, k, v, lens, q, hd ** -0.5 if scale is None else scale)
+    got = out.cpu()
+    check(got[:-1], want, tol, max(float(x.abs().max()) for x in v))
+    assert bool((got[-1] == 7.5).all())
+    return max(lens)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("case", CASES, ids=IDS)
 def test_paths(case, fp8):
     nq, nkv, hd, block, q, sizes, prefixes, own, layout, way = case
     print(f"[gpu] prefix path {case} {fp8}", flush=True)
-    g = torch.Generator().manual_seed(nq + sum(sizes))
     rng, mine, top = sizes_of(case)
-    B = sum(sizes)
-    c, table, lens, k, v = shared(g, sizes, prefixes, mine, nkv, hd, block, layout, fp8, rng)
-    assert max(lens) == top
-    query = randn(g, B * q, nq * hd)
-    out = torch.full((B * q + 1, nq * hd), 7.5, dtype=BF16, device="cuda")
-    fn = scs().sc_paged_attn_prefix_fp8 if fp8 else scs().sc_paged_attn_prefix
-    fn(query.cuda(), out, *c, i32(table), i32(lens), i32(np.concatenate([[0], np.cumsum(sizes)])),
-       i32(prefixes), q=q, max_seq_len=int(top), max_prefix_len=max(prefixes))
-    want, tol = attn_ref(query, k, v, lens, q, hd ** -0.5)
-    got = out.cpu()
-    check(got[:-1], want, tol, max(float(x.abs().max()) for x in v))
-    assert bool((got[-1] == 7.5).all())
+    assert run(fp8, nq, nkv, hd, block, q, sizes, prefixes, mine, layout, None, rng, nq + sum(sizes)) == top
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("case", SMALL, ids=[f"{c[0]}-{c[1]}-{c[2]}-q{c[4]}-{c[5][0]}on{c[6][0]}" for c in SMALL])
+def test_small_cases_by_mean_square(case, fp8):
+    nq, nkv, hd, block, q, sizes, prefixes, own, layout, scale = case
+    print(f"[gpu] prefix mean square {case} {fp8}", flush=True)
+    rng = np.random.default_rng(hd + 1)
+    run(fp8, nq, nkv, hd, block, q, sizes, prefixes, rng.integers(own[0], own[1] + 1, sum(sizes)), layout,
+        scale, rng, nq)
 
 
 @pytest.mark.gpu
