@@ -486,8 +486,9 @@ typedef struct {
 /* sc_qk_norm_rope into a quantised cache (required here). The scale of a head is the
  * smallest power of two, from 2^-126 on, that brings its largest finite value to 448
  * or less; values over it are rounded to the nearest code, ties to even, keys
- * straight from fp64. Infinities and NaN become NaN codes and leave the scale to
- * the others. Codes 4-byte aligned, strides a multiple of 4. */
+ * straight from fp64. Infinities, keys past fp32's range among them, and NaN become
+ * NaN codes and leave the scale to the others. Codes 4-byte aligned, strides a
+ * multiple of 4. */
 sc_status sc_qk_norm_rope_fp8(const sc_qk_norm_desc* desc, const void* q, const void* k,
                               const void* v, void* q_out, void* k_out, const void* q_weight,
                               const void* k_weight, const void* cos_sin, const int64_t* positions,

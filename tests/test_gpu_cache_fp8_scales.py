@@ -27,3 +27,25 @@ def test_every_code_and_scale():
     want = torch.where(want.abs() >= 2.0 ** 128, torch.copysign(torch.tensor(float("inf"), dtype=F64), want), want)
     for out in (ko, vo):
         assert torch.equal(out.cpu().to(F64)[:255].nan_to_num(nan=3.5), want[:255].nan_to_num(nan=3.5))
+
+
+def test_keys_past_fp32():
+    """A normalised key of sqrt(64) times a weight of 2^126 passes 2^128: a NaN code, and the
+    others, 2^-20 of it, have the scale of the largest that is left."""
+    print("[gpu] keys past fp32", flush=True)
+    hd = 64
+    k = torch.full((1, hd), 2.0 ** -20, dtype=BF16)
+    k[0, 5] = 1.0
+    w = torch.full((hd,), 2.0 ** 126, dtype=BF16)
+    q = torch.zeros(1, hd, dtype=BF16, device="cuda")
+    c = [torch.zeros(1, 1, 1, hd, dtype=U8, device="cuda").view(E4M3), torch.zeros(1, 1, 1, dtype=U8, device="cuda"),
+         torch.zeros(1, 1, 1, hd, dtype=U8, device="cuda").view(E4M3), torch.zeros(1, 1, 1, dtype=U8, device="cuda")]
+    scs().sc_qk_norm_rope_fp8(q, k.cuda(), q, torch.empty_like(q), None, None, w.cuda(), None, None,
+                              torch.zeros(1, dtype=torch.int64, device="cuda"), *c, head_dim=hd, eps=0.0)
+    x = k[0].to(F64)
+    x = x / x.square().mean().sqrt() * 2.0 ** 126
+    got = CODES[c[0].view(U8).cpu().view(-1).long()] * 2.0 ** (int(c[1]) - 127)
+    rest = torch.arange(hd) != 5
+    assert bool(got[5].isnan()) and bool(x[5] >= 2.0 ** 128)
+    # one rounding to four significant bits, and the byte is of these alone: 2^109 = 256 2^101
+    assert bool(((got[rest] - x[rest]).abs() <= 2.0 ** -4 * x[rest]).all()) and int(c[1]) == 101 + 127
